@@ -105,8 +105,12 @@ enum {
   PQKV_DEVERR_TIMEOUT = 16,  /* a bounded wait on an asynchronous copy gave up; the kernel's
                                 remaining work for that warp is skipped (outputs it owns are
                                 left unwritten) after its copies in flight have landed */
-  PQKV_DEVERR_DRAIN = 32     /* after a TIMEOUT, a copy still in flight did not land within the
+  PQKV_DEVERR_DRAIN = 32,    /* after a TIMEOUT, a copy still in flight did not land within the
                                 full wait limit either */
+  PQKV_DEVERR_CAPACITY = 64, /* batch: a request's tokens or new blocks pass what the call has room
+                                for; it and every request behind it are left out */
+  PQKV_DEVERR_POSITION = 128 /* rotary: a position outside the table of cosines and sines; the
+                                token's query and key rows are written as zeros */
 };
 
 #define PQKV_BLOCK_SIZE 16
@@ -326,6 +330,32 @@ int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_
                                  void* out, int32_t* err_flag, pqkv_stream_t stream);
 
 /*
+ * Attention to an encoder's states over the paged cache: decoder tokens read
+ * keys and values of another length than their own, written once
+ * (pqkv_kv_cache_write) and kept ([P3] "PagedAttention": one copy in several
+ * block tables). Sequence b's query tokens are rows cu_q_lens[b] ..
+ * cu_q_lens[b+1]-1 of q, any number of them, and its states positions 0 ..
+ * kv_lens[b]-1 through its block table; every token sees all of them, or, with
+ * kv_ranges (device int32 [cu_q_lens[batch]][2], 8-byte aligned; NULL = none),
+ * positions [kv_ranges[t][0], kv_ranges[t][1]) cut to [0, kv_lens[b]): the
+ * pictures before a token, say. out_row = softmax(scale * q K^T) V over what
+ * the token sees; a token that sees nothing (no states, or an empty range) gets
+ * a zero row. Rows of q behind cu_q_lens[batch] are not touched. Other
+ * arguments, results and errors as in pqkv_paged_prefill_attention (a
+ * kv_lens[b] below 0 or above 16 * max_blocks_per_seq gives zero rows and
+ * PQKV_DEVERR_SEQ_LEN). One kernel on `stream`, on the tensor cores (tcgen05);
+ * no workspace. With one token in each of `batch` sequences and no ranges
+ * pqkv_paged_decode_attention computes the same.
+ */
+int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
+                               const int32_t* cu_q_lens, const void* cache, const void* scales,
+                               const void* outliers_idx, const void* outliers_val, int kv_dtype,
+                               int num_blocks, int num_kv_heads, int head_dim,
+                               const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* kv_lens, const int32_t* kv_ranges, float scale, void* out,
+                               int32_t* err_flag, pqkv_stream_t stream);
+
+/*
  * Whole-block copy for copy-on-write ([P3] PagedAttention: blocks shared across
  * sequences for beam search and parallel sampling; a sequence that forks off a
  * shared partial block writes into its own copy). pairs: device int32
@@ -365,6 +395,92 @@ int pqkv_swap_in(void* cache, void* scales, void* outliers_idx, void* outliers_v
                  int kv_dtype, int num_blocks, int num_kv_heads, int head_dim,
                  const int32_t* block_ids, int num, const void* host_records,
                  int32_t* err_flag, pqkv_stream_t stream);
+
+/*
+ * The tables of a batch, on the GPU, from request lengths that are there already
+ * ([P3] "PagedAttention": logical to physical blocks; "Continuous batching":
+ * every iteration has another batch): the device form of pqkv_build_slot_mapping,
+ * with the block tables' growth and the offsets that the attention calls take.
+ * Request b has start_pos[b] tokens in the cache and adds num_new[b] (device
+ * int32 [batch] each; 0 is allowed in both). new_block_ids (device int32
+ * [num_new_blocks], as pqkv_pool_alloc hands them out) holds the ids of the
+ * blocks that the step adds, request after request: request b takes the next
+ * ceil((start + new) / 16) - ceil(start / 16). Results:
+ *   block_tables [batch][max_blocks_per_seq], in place: row b gains its new ids
+ *     behind its first ceil(start / 16) entries; all others stay as they are
+ *   slot_mapping [max_tokens]: slots of the new tokens, request after request;
+ *     -1 (skipped by pqkv_kv_cache_write) behind the last one
+ *   positions [max_tokens]: their positions in their sequences; 0 behind the last
+ *   cu_q_lens [batch + 1]: offsets of the requests' tokens
+ *   seq_lens [batch]: start_pos + num_new
+ * A request with a negative length, or more than 16 * max_blocks_per_seq tokens
+ * in all, sets PQKV_DEVERR_SEQ_LEN and counts as empty (seq_lens 0, no tokens).
+ * The first request whose tokens pass max_tokens or whose blocks pass
+ * num_new_blocks sets PQKV_DEVERR_CAPACITY; it and all behind it get no tokens,
+ * no blocks and seq_lens 0. An id outside [0, num_blocks), in new_block_ids or
+ * in the table entry of a request's open block, sets PQKV_DEVERR_BLOCK_ID; its
+ * tokens get slot -1 and a new one's table entry is -1. A table row belongs to
+ * one request; the arrays must not overlap. batch <= PQKV_MAX_BATCH. One kernel
+ * on `stream`; no workspace.
+ */
+int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch,
+                     const int32_t* new_block_ids, int num_new_blocks, int32_t* block_tables,
+                     int max_blocks_per_seq, int num_blocks, int max_tokens, int32_t* slot_mapping,
+                     int32_t* positions, int32_t* cu_q_lens, int32_t* seq_lens, int32_t* err_flag,
+                     pqkv_stream_t stream);
+
+/*
+ * RMS norm of every query and key head and rotary positions, in one pass over
+ * the projection's output, which precedes the cache write and the attention (the
+ * pages take K and V as given). Row x (one head of one token, head_dim
+ * channels): y = x / sqrt(mean(x^2) + eps) * weight, in fp32 (finite rows of
+ * |x| < 2^60), with q_weight or k_weight (device float [head_dim]; NULL = no
+ * norm of those rows). Then, with r = rot_dim / 2, pair i < r of the first
+ * rot_dim channels turns by the token's position on the pair's axis:
+ *   p = positions[axis_of_pair[i]][token], c = cos_sin[p][i], s = cos_sin[p][r + i]
+ *   (a, b) -> (a c - b s, b c + a s)
+ * on channels i and i + r (interleaved = 0) or 2i and 2i + 1 (interleaved = 1);
+ * channels from rot_dim on are not turned. The result is rounded once.
+ * q, k: device arrays of `dtype` (FP16 or BF16), heads of a token contiguous
+ * ([num_heads][head_dim]), q_stride / k_stride elements from one token to the
+ * next (multiples of 8, at least one token's heads): parts of a fused
+ * projection's output. q_out, k_out: [num_tokens][heads][head_dim] contiguous;
+ * either may be its input if that is contiguous too, other overlaps are
+ * PQKV_ERR_ARG. num_kv_heads = 0: queries only (k and k_out unused).
+ * positions: device int32 [num_axes][num_tokens], 1 <= num_axes <= 4.
+ * axis_of_pair: host bytes [rot_dim / 2] below num_axes, or NULL (all axis 0).
+ * cos_sin: device float [num_positions][rot_dim], cosines then sines of a
+ * position's pairs (the caller fills it once, for its frequencies and scaling).
+ * rot_dim: a multiple of 8 from 0 (no rotation; positions and cos_sin unused)
+ * to head_dim (64 or 128). A position outside [0, num_positions) sets
+ * PQKV_DEVERR_POSITION and zeros the token's rows. q, k, the outputs, cos_sin
+ * and the weights are 16-byte aligned. One kernel on `stream`.
+ */
+int pqkv_qk_norm_rope(const void* q, const void* k, int dtype, int num_tokens, int num_q_heads,
+                      int num_kv_heads, int head_dim, int64_t q_stride, int64_t k_stride,
+                      const float* q_weight, const float* k_weight, float eps,
+                      const int32_t* positions, int num_axes, const uint8_t* axis_of_pair,
+                      const float* cos_sin, int num_positions, int rot_dim, int interleaved,
+                      void* q_out, void* k_out, int32_t* err_flag, pqkv_stream_t stream);
+
+/*
+ * pqkv_qk_norm_rope and pqkv_kv_cache_write in one call: the queries go to q_out
+ * as there, and the keys (normed, turned and rounded to `dtype`) and the values
+ * (as they are) to the slots of slot_mapping as if written by
+ * pqkv_kv_cache_write, without a contiguous copy of either in between; the
+ * results are the same, bit for bit. v: as k, v_stride elements from one token
+ * to the next. num_kv_heads >= 1; other arguments, rules on runs and errors as
+ * in the two calls (a token whose position lies outside the table has a zero
+ * key). 16-bit caches: one kernel; FP8 and FP4: two.
+ */
+int pqkv_qkv_norm_rope_write(const void* q, const void* k, const void* v, int dtype, int num_tokens,
+                             int num_q_heads, int num_kv_heads, int head_dim, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float* q_weight,
+                             const float* k_weight, float eps, const int32_t* positions, int num_axes,
+                             const uint8_t* axis_of_pair, const float* cos_sin, int num_positions,
+                             int rot_dim, int interleaved, void* q_out, const int32_t* slot_mapping,
+                             void* cache, void* scales, void* outliers_idx, void* outliers_val,
+                             int kv_dtype, int num_blocks, int32_t* err_flag, pqkv_stream_t stream);
 
 /* Zero-fill a decode workspace on `stream`. Optional: it only removes the
  * chance (about 2^-40 per split pair) that a never-used buffer's arbitrary old

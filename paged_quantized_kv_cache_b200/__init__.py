@@ -26,6 +26,7 @@ DTYPE_NAMES = {FP16: "fp16", BF16: "bf16", FP8_E4M3: "fp8_e4m3", FP8_E5M2: "fp8_
 OK, ERR_ARG, ERR_OOM, ERR_STATE, ERR_CUDA, ERR_SCRATCH = 0, 1, 2, 3, 4, 5
 NOALLOC_SCRATCH_BYTES = 16 << 20
 DEVERR_SLOT, DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_RUN, DEVERR_TIMEOUT, DEVERR_DRAIN = 1, 2, 4, 8, 16, 32
+DEVERR_CAPACITY, DEVERR_POSITION = 64, 128
 BLOCK_SIZE = 16
 MAX_BATCH = 4096
 
@@ -39,7 +40,8 @@ EXPORTS = (
     "pqkv_pool_prefix_lookup", "pqkv_pool_prefix_insert", "pqkv_pool_cow", "pqkv_copy_blocks",
     "pqkv_block_record_bytes", "pqkv_swap_out", "pqkv_swap_in", "pqkv_paged_prefill_attention",
     "pqkv_paged_multi_query_decode_attention", "pqkv_multi_query_decode_workspace_bytes",
-    "pqkv_read_probe", "pqkv_set_decode_wait_limit_ns",
+    "pqkv_read_probe", "pqkv_set_decode_wait_limit_ns", "pqkv_build_batch", "pqkv_qk_norm_rope",
+    "pqkv_qkv_norm_rope_write", "pqkv_paged_cross_attention",
 )
 
 
@@ -54,6 +56,7 @@ def _load() -> ctypes.CDLL:
         raise ImportError("libpqkv.so is not built (run: python -m paged_quantized_kv_cache_b200.build)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    L, F = ctypes.c_int64, ctypes.c_float
     sig = {
         "pqkv_version": (I, []),
         "pqkv_status_string": (ctypes.c_char_p, [I]),
@@ -90,6 +93,11 @@ def _load() -> ctypes.CDLL:
                                                         ctypes.c_float, I, P, P, Z, P, P]),
         "pqkv_read_probe": (I, [P, I, I, I, I, P, I, P, I, P, P, P]),
         "pqkv_set_decode_wait_limit_ns": (None, [ctypes.c_uint64]),
+        "pqkv_paged_cross_attention": (I, [P, I, I, I, I, P, P, P, P, P, I, I, I, I, P, I, P, P, F, P, P, P]),
+        "pqkv_build_batch": (I, [P, P, I, P, I, P, I, I, I, P, P, P, P, P, P]),
+        "pqkv_qk_norm_rope": (I, [P, P, I, I, I, I, I, L, L, P, P, F, P, I, ctypes.c_char_p, P, I, I, I, P, P, P, P]),
+        "pqkv_qkv_norm_rope_write": (I, [P, P, P, I, I, I, I, I, L, L, L, P, P, F, P, I, ctypes.c_char_p, P, I, I, I,
+                                         P, P, P, P, P, P, I, I, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -311,6 +319,183 @@ def paged_prefill_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len:
         ctypes.c_float(scale), _dev_ptr(out, "out"), _dev_ptr(err_flag, "err_flag"),
         _stream_handle(stream, q.device))
     _check("pqkv_paged_prefill_attention", st)
+
+
+class _OnDevice:
+    """Pointers of a call's tensors, all on one device, which is current while the library is called."""
+
+    def __init__(self, t: torch.Tensor, name: str):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        self.index = t.get_device()
+
+    def ptr(self, t: Optional[torch.Tensor], name: str, dtype: Optional[torch.dtype] = None,
+            contiguous: bool = True) -> Optional[int]:
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
+            raise ValueError("%s must be a tensor on cuda:%d" % (name, self.index))
+        if dtype is not None and t.dtype != dtype:
+            raise ValueError("%s must be %s" % (name, dtype))
+        if contiguous and not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        return t.data_ptr()
+
+    def cache(self, c: KVCache):
+        return (self.ptr(c.cache, "cache"), self.ptr(c.scales, "scales"), self.ptr(c.outliers_idx, "outliers_idx"),
+                self.ptr(c.outliers_val, "outliers_val"))
+
+    def call(self, func: str, stream, *args) -> None:
+        if stream is None:
+            stream = torch.cuda.current_stream(self.index)
+        if torch.cuda.current_device() == self.index:
+            st = getattr(lib(), func)(*args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.index):
+                st = getattr(lib(), func)(*args, stream.cuda_stream)
+        _check(func, st)
+
+
+def paged_cross_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: int, cache: KVCache,
+                          block_tables: torch.Tensor, kv_lens: torch.Tensor, scale: float, out: torch.Tensor,
+                          err_flag: torch.Tensor, kv_ranges: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pqkv_paged_cross_attention: q, out [T][Hq][D]; cu_q_lens int32 [B + 1]; block_tables int32
+    [B][max_blocks] and kv_lens int32 [B] of the encoder's states; kv_ranges int32 [T][2] or None."""
+    dev = _OnDevice(q, "q")
+    i32 = torch.int32
+    T, Hq, D = q.shape
+    B = kv_lens.numel()
+    if out.shape != q.shape or D != cache.head_dim:
+        raise ValueError("out must match q, and q the cache's head_dim")
+    if cu_q_lens.numel() != B + 1:
+        raise ValueError("cu_q_lens must be int32 [B + 1]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [B][max_blocks_per_seq]")
+    if kv_ranges is not None and kv_ranges.shape != (T, 2):
+        raise ValueError("kv_ranges must be int32 [T][2]")
+    if T == 0:
+        return
+    dev.call("pqkv_paged_cross_attention", stream, dev.ptr(q, "q"), _dt_of(q, "q"), B, max_q_len, Hq,
+             dev.ptr(cu_q_lens, "cu_q_lens", i32), *dev.cache(cache), cache.kv_dtype, cache.num_blocks,
+             cache.num_kv_heads, D, dev.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
+             dev.ptr(kv_lens, "kv_lens", i32), dev.ptr(kv_ranges, "kv_ranges", i32), scale,
+             dev.ptr(out, "out", q.dtype), dev.ptr(err_flag, "err_flag", i32))
+
+
+def build_batch(start_pos: torch.Tensor, num_new: torch.Tensor, new_block_ids: torch.Tensor,
+                block_tables: torch.Tensor, num_blocks: int, slot_mapping: torch.Tensor, positions: torch.Tensor,
+                cu_q_lens: torch.Tensor, seq_lens: torch.Tensor, err_flag: torch.Tensor, stream=None) -> None:
+    """pqkv_build_batch: start_pos, num_new int32 [B] and new_block_ids int32 [n] on the device -> block_tables
+    int32 [B][max_blocks] (in place), slot_mapping and positions int32 [max_tokens], cu_q_lens int32 [B + 1],
+    seq_lens int32 [B]."""
+    dev = _OnDevice(start_pos, "start_pos")
+    i32 = torch.int32
+    B = start_pos.numel()
+    if num_new.numel() != B or seq_lens.numel() != B or cu_q_lens.numel() != B + 1:
+        raise ValueError("num_new and seq_lens must be [B], cu_q_lens [B + 1]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [B][max_blocks_per_seq]")
+    if positions.numel() != slot_mapping.numel():
+        raise ValueError("positions and slot_mapping must be of one size")
+    dev.call("pqkv_build_batch", stream, dev.ptr(start_pos, "start_pos", i32), dev.ptr(num_new, "num_new", i32), B,
+             dev.ptr(new_block_ids, "new_block_ids", i32), new_block_ids.numel(),
+             dev.ptr(block_tables, "block_tables", i32), block_tables.shape[1], num_blocks, slot_mapping.numel(),
+             dev.ptr(slot_mapping, "slot_mapping", i32), dev.ptr(positions, "positions", i32),
+             dev.ptr(cu_q_lens, "cu_q_lens", i32), dev.ptr(seq_lens, "seq_lens", i32),
+             dev.ptr(err_flag, "err_flag", i32))
+
+
+@dataclasses.dataclass
+class Rotary:
+    """Rotary positions: float32 [num_positions][rot_dim] (cosines of a position's rot_dim / 2 pairs, then their
+    sines), the axis of each pair (one byte each; empty = all on axis 0) and whether pairs are neighbouring
+    channels (2i, 2i + 1) or halves (i, i + rot_dim / 2)."""
+    cos_sin: torch.Tensor
+    axis_of_pair: bytes = b""
+    interleaved: bool = False
+
+
+def _heads(dev: _OnDevice, x: torch.Tensor, name: str, T: int, D: int, dtype: torch.dtype) -> Tuple[int, int]:
+    """Pointer and token stride of [T][H][D] rows whose heads are contiguous within a token."""
+    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.stride(2) != 1 or \
+            (x.stride(1) != D and x.shape[1] > 1):
+        raise ValueError("%s must be [T][heads][head_dim] with contiguous heads" % name)
+    # the stride of a dimension of one token means nothing
+    return dev.ptr(x, name, dtype, contiguous=False), (x.stride(0) if T > 1 else x.shape[1] * D)
+
+
+def _rotary_args(dev: _OnDevice, rotary: Optional[Rotary], positions: Optional[torch.Tensor], T: int):
+    """positions, num_axes, axis_of_pair, cos_sin, num_positions, rot_dim, interleaved."""
+    if rotary is None:
+        return None, 0, None, None, 0, 0, 0
+    table = rotary.cos_sin
+    if table.dim() != 2:
+        raise ValueError("cos_sin must be float32 [num_positions][rot_dim]")
+    rot = table.shape[1]
+    if rotary.axis_of_pair and len(rotary.axis_of_pair) != rot // 2:
+        raise ValueError("axis_of_pair must hold rot_dim / 2 bytes")
+    axes = 1
+    if rot:
+        if positions is None or positions.dim() not in (1, 2) or positions.shape[-1] != T:
+            raise ValueError("positions must be int32 [T] or [axes][T]")
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+    return (dev.ptr(positions, "positions", torch.int32), axes, rotary.axis_of_pair or None,
+            dev.ptr(table, "cos_sin", torch.float32), table.shape[0], rot, int(rotary.interleaved))
+
+
+def _weight(dev: _OnDevice, w: Optional[torch.Tensor], name: str, D: int) -> Optional[int]:
+    if w is not None and w.numel() != D:
+        raise ValueError("%s must be float32 [head_dim]" % name)
+    return dev.ptr(w, name, torch.float32)
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                 rotary: Optional[Rotary], q_out: torch.Tensor, k_out: Optional[torch.Tensor],
+                 err_flag: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
+    """pqkv_qk_norm_rope: q [T][Hq][D] and k [T][Hkv][D] (or None), the heads of a token contiguous, any stride
+    from one token to the next; positions int32 [T] or [axes][T]; q_out, k_out contiguous, or the input itself.
+    A weight of None leaves the norm out, a rotary of None the rotation."""
+    dev = _OnDevice(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T][num_q_heads][head_dim]")
+    T, Hq, D = q.shape
+    dt = _dt_of(q, "q")
+    if q_out.shape != q.shape or (k is None) != (k_out is None) or (k is not None and k_out.shape != k.shape):
+        raise ValueError("q_out and k_out must match q and k")
+    qp, qs = _heads(dev, q, "q", T, D, q.dtype)
+    kp, ks = _heads(dev, k, "k", T, D, q.dtype) if k is not None else (None, 0)
+    dev.call("pqkv_qk_norm_rope", stream, qp, kp, dt, T, Hq, k.shape[1] if k is not None else 0, D, qs, ks,
+             _weight(dev, q_weight, "q_weight", D), _weight(dev, k_weight, "k_weight", D), eps,
+             *_rotary_args(dev, rotary, positions, T), dev.ptr(q_out, "q_out", q.dtype),
+             dev.ptr(k_out, "k_out", q.dtype), dev.ptr(err_flag, "err_flag", torch.int32))
+
+
+def qkv_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
+                        rotary: Optional[Rotary], q_out: torch.Tensor, slot_mapping: torch.Tensor, cache: KVCache,
+                        err_flag: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
+    """pqkv_qkv_norm_rope_write: qk_norm_rope whose keys, with the values v [T][Hkv][D], go to the cache slots
+    of slot_mapping int32 [T] as kv_cache_write would store them."""
+    dev = _OnDevice(q, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [T][num_q_heads][head_dim]")
+    T, Hq, D = q.shape
+    dt = _dt_of(q, "q")
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must match q")
+    if k.shape != (T, cache.num_kv_heads, cache.head_dim) or v.shape != k.shape or D != cache.head_dim:
+        raise ValueError("k and v must be [T][num_kv_heads][head_dim]")
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must be int32 [T]")
+    qp, qs = _heads(dev, q, "q", T, D, q.dtype)
+    kp, ks = _heads(dev, k, "k", T, D, q.dtype)
+    vp, vs = _heads(dev, v, "v", T, D, q.dtype)
+    dev.call("pqkv_qkv_norm_rope_write", stream, qp, kp, vp, dt, T, Hq, k.shape[1], D, qs, ks, vs,
+             _weight(dev, q_weight, "q_weight", D), _weight(dev, k_weight, "k_weight", D), eps,
+             *_rotary_args(dev, rotary, positions, T), dev.ptr(q_out, "q_out", q.dtype),
+             dev.ptr(slot_mapping, "slot_mapping", torch.int32), *dev.cache(cache), cache.kv_dtype,
+             cache.num_blocks, dev.ptr(err_flag, "err_flag", torch.int32))
 
 
 def encode(x: torch.Tensor, code_dtype: int, out: torch.Tensor, stream=None) -> None:

@@ -3,12 +3,15 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
+#include "batch.cuh"
 #include "blocks.cuh"
 #include "decode.cuh"
 #include "prefill.cuh"
+#include "rope.cuh"
 #include "write.cuh"
 
 namespace pqkv {
@@ -127,6 +130,67 @@ bool cached_cache_map(CUtensorMap* map, const void* cache, int kv_dtype, int nb,
   return true;
 }
 
+// Whether bytes [a, a + na) and [b, b + nb) share any.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// One operand of the rotary calls: rows of `heads` heads of D 16-bit channels,
+// `stride` elements from one token to the next.
+struct Heads {
+  const void* p;
+  int heads;
+  int64_t stride;
+  size_t bytes(int T, int D) const { return ((size_t)(T - 1) * (size_t)stride + (size_t)heads * D) * 2; }
+};
+
+// Checks of the norm and rotation shared by both rotary calls; fills r.
+int rope_params(RowParams& r, int dtype, int T, int Hq, int D, const float* qw, const float* kw, float eps,
+                const int32_t* positions, int axes, const uint8_t* axis_of_pair, const float* cos_sin, int num_pos,
+                int rot, int interleaved) {
+  if ((dtype != PQKV_DTYPE_FP16 && dtype != PQKV_DTYPE_BF16) || T < 0 || Hq < 1 || (D != 64 && D != 128) ||
+      rot < 0 || rot > D || rot % 8 != 0 || (interleaved != 0 && interleaved != 1) || !(eps >= 0.f))
+    return PQKV_ERR_ARG;
+  if (rot > 0 && (axes < 1 || axes > kMaxAxes || num_pos < 1)) return PQKV_ERR_ARG;
+  std::memset(&r, 0, sizeof(r));
+  if (rot > 0 && axis_of_pair) {
+    for (int i = 0; i < rot / 2; ++i) {
+      if (axis_of_pair[i] >= axes) return PQKV_ERR_ARG;
+      r.axis[i / 4] |= (uint32_t)axis_of_pair[i] << (8 * (i % 4));
+    }
+  }
+  if (T > 0 && rot > 0 && (!positions || !cos_sin || !aligned16(cos_sin))) return PQKV_ERR_ARG;
+  if ((qw && !aligned16(qw)) || (kw && !aligned16(kw))) return PQKV_ERR_ARG;
+  r.q_weight = qw;
+  r.k_weight = kw;
+  r.positions = positions;
+  r.cos_sin = cos_sin;
+  r.eps = eps;
+  r.T = T;
+  r.num_pos = num_pos;
+  r.rot = rot;
+  r.axes = axes;
+  return PQKV_OK;
+}
+
+bool heads_ok(const Heads& x, int D) {
+  return x.p && aligned16(x.p) && x.stride >= (int64_t)x.heads * D && x.stride % 8 == 0;
+}
+
+// An output may be its own input where both lie the same way (each row is read
+// before it is written, by the same lanes), and touches nothing else.
+bool out_ok(const Heads& out, const Heads* in, int n_in, int own, int T, int D) {
+  for (int i = 0; i < n_in; ++i) {
+    if (!in[i].p || !overlap(out.p, out.bytes(T, D), in[i].p, in[i].bytes(T, D))) continue;
+    if (i != own || out.p != in[i].p || (T > 1 && in[i].stride != out.stride)) return false;
+  }
+  return true;
+}
+
+// CTAs of the rotary kernel fit a grid (8 warps of at least 8 rows of a token each).
+bool rope_grid_ok(int64_t T, int64_t rows) { return T * ((rows + 7) / 8) / 8 < INT32_MAX - 8; }
+
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Workspace = two partial-result slots per chunk of the split and one arrival
@@ -200,6 +264,7 @@ int pqkv_kv_cache_write(const void* k, const void* v, int in_dtype, int num_toke
   if (!is_16(kv_dtype) && !scales) return PQKV_ERR_ARG;
   if (kv_dtype == PQKV_DTYPE_FP4_E2M1 && (!outliers_idx || !outliers_val)) return PQKV_ERR_ARG;
   WriteParams p;
+  std::memset(&p, 0, sizeof(p));
   p.k = k;
   p.v = v;
   p.slots = slot_mapping;
@@ -427,12 +492,12 @@ int pqkv_swap_in(void* cache, void* scales, void* outliers_idx, void* outliers_v
                     head_dim, block_ids, num, const_cast<void*>(host_records), err_flag, stream);
 }
 
-int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
-                                 const int32_t* cu_q_lens, const void* cache, const void* scales,
-                                 const void* outliers_idx, const void* outliers_val, int kv_dtype, int num_blocks,
-                                 int num_kv_heads, int head_dim, const int32_t* block_tables,
-                                 int max_blocks_per_seq, const int32_t* seq_lens, float scale, void* out,
-                                 int32_t* err_flag, pqkv_stream_t stream) {
+// The checks and parameters that the prefill and the cross attention share.
+static int prefill_impl(bool cross, const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
+                        const int32_t* cu_q_lens, const void* cache, const void* scales, const void* outliers_idx,
+                        const void* outliers_val, int kv_dtype, int num_blocks, int num_kv_heads, int head_dim,
+                        const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                        const int32_t* ranges, float scale, void* out, int32_t* err_flag, pqkv_stream_t stream) {
   if (!is_kv_dtype(kv_dtype) || (q_dtype != PQKV_DTYPE_FP16 && q_dtype != PQKV_DTYPE_BF16)) return PQKV_ERR_ARG;
   if (is_16(kv_dtype) && q_dtype != kv_dtype) return PQKV_ERR_ARG;
   if (batch < 0 || max_q_len < 1 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 ||
@@ -479,8 +544,176 @@ int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = g_decode_wait_ns.load();
   p.drain_ns = kWaitLimitNs;
-  const cudaError_t e = launch_prefill(kv_dtype, head_dim, q_dtype == PQKV_DTYPE_BF16, tmap, p,
-                                       reinterpret_cast<cudaStream_t>(stream));
+  p.ranges = ranges;
+  p.splits = 1;
+  p.q_and = 0xFFFFFFFFu;
+  p.q_xor = 0;
+  if (cross && scale < 0.f) {
+    p.q_xor = 0x80008000u;
+    p.scale_log2 = -p.scale_log2;
+  } else if (cross && scale == 0.f) {
+    p.q_and = 0;
+    p.scale_log2 = 1.f;
+  }
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool q_bf16 = q_dtype == PQKV_DTYPE_BF16;
+  const cudaError_t e = cross ? launch_cross(kv_dtype, head_dim, q_bf16, tmap, p, di.sms, st)
+                              : launch_prefill(kv_dtype, head_dim, q_bf16, tmap, p, st);
+  return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
+}
+
+int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
+                                 const int32_t* cu_q_lens, const void* cache, const void* scales,
+                                 const void* outliers_idx, const void* outliers_val, int kv_dtype, int num_blocks,
+                                 int num_kv_heads, int head_dim, const int32_t* block_tables,
+                                 int max_blocks_per_seq, const int32_t* seq_lens, float scale, void* out,
+                                 int32_t* err_flag, pqkv_stream_t stream) {
+  return prefill_impl(false, q, q_dtype, batch, max_q_len, num_q_heads, cu_q_lens, cache, scales, outliers_idx,
+                      outliers_val, kv_dtype, num_blocks, num_kv_heads, head_dim, block_tables, max_blocks_per_seq,
+                      seq_lens, nullptr, scale, out, err_flag, stream);
+}
+
+int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
+                               const int32_t* cu_q_lens, const void* cache, const void* scales,
+                               const void* outliers_idx, const void* outliers_val, int kv_dtype, int num_blocks,
+                               int num_kv_heads, int head_dim, const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* kv_lens, const int32_t* kv_ranges, float scale, void* out,
+                               int32_t* err_flag, pqkv_stream_t stream) {
+  if ((reinterpret_cast<uintptr_t>(kv_ranges) & 7u) != 0 || !std::isfinite(scale)) return PQKV_ERR_ARG;
+  return prefill_impl(true, q, q_dtype, batch, max_q_len, num_q_heads, cu_q_lens, cache, scales, outliers_idx,
+                      outliers_val, kv_dtype, num_blocks, num_kv_heads, head_dim, block_tables, max_blocks_per_seq,
+                      kv_lens, kv_ranges, scale, out, err_flag, stream);
+}
+
+int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch, const int32_t* new_block_ids,
+                     int num_new_blocks, int32_t* block_tables, int max_blocks_per_seq, int num_blocks,
+                     int max_tokens, int32_t* slot_mapping, int32_t* positions, int32_t* cu_q_lens,
+                     int32_t* seq_lens, int32_t* err_flag, pqkv_stream_t stream) {
+  if (batch < 1 || batch > PQKV_MAX_BATCH || num_new_blocks < 0 || max_blocks_per_seq < 1 ||
+      max_blocks_per_seq > INT32_MAX / PQKV_BLOCK_SIZE || num_blocks < 1 || max_tokens < 0)
+    return PQKV_ERR_ARG;
+  if ((int64_t)num_blocks * PQKV_BLOCK_SIZE > INT32_MAX) return PQKV_ERR_ARG;
+  if (!start_pos || !num_new || (num_new_blocks > 0 && !new_block_ids) || !block_tables ||
+      (max_tokens > 0 && (!slot_mapping || !positions)) || !cu_q_lens || !seq_lens || !err_flag)
+    return PQKV_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(di)) return PQKV_ERR_CUDA;
+  BatchParams p;
+  p.start = start_pos;
+  p.num_new = num_new;
+  p.ids = new_block_ids;
+  p.tables = block_tables;
+  p.slots = slot_mapping;
+  p.positions = positions;
+  p.cu = cu_q_lens;
+  p.lens = seq_lens;
+  p.err = err_flag;
+  p.B = batch;
+  p.n_ids = num_new_blocks;
+  p.maxblk = max_blocks_per_seq;
+  p.nb = num_blocks;
+  p.cap = max_tokens;
+  const cudaError_t e = launch_build_batch(p, di.sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
+}
+
+int pqkv_qk_norm_rope(const void* q, const void* k, int dtype, int num_tokens, int num_q_heads, int num_kv_heads,
+                      int head_dim, int64_t q_stride, int64_t k_stride, const float* q_weight,
+                      const float* k_weight, float eps, const int32_t* positions, int num_axes,
+                      const uint8_t* axis_of_pair, const float* cos_sin, int num_positions, int rot_dim,
+                      int interleaved, void* q_out, void* k_out, int32_t* err_flag, pqkv_stream_t stream) {
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int T = num_tokens, D = head_dim;
+  if (rope_params(p.r, dtype, T, num_q_heads, D, q_weight, k_weight, eps, positions, num_axes, axis_of_pair, cos_sin,
+                  num_positions, rot_dim, interleaved) != PQKV_OK ||
+      num_kv_heads < 0 || !rope_grid_ok(T, (int64_t)num_q_heads + num_kv_heads))
+    return PQKV_ERR_ARG;
+  if (T == 0) return PQKV_OK;
+  const Heads in[2] = {{q, num_q_heads, q_stride}, {num_kv_heads ? k : nullptr, num_kv_heads, k_stride}};
+  const Heads qo{q_out, num_q_heads, (int64_t)num_q_heads * D}, ko{k_out, num_kv_heads, (int64_t)num_kv_heads * D};
+  if (!err_flag || !heads_ok(in[0], D) || !heads_ok(qo, D) || !out_ok(qo, in, 2, 0, T, D)) return PQKV_ERR_ARG;
+  if (num_kv_heads &&
+      (!heads_ok(in[1], D) || !heads_ok(ko, D) || !out_ok(ko, in, 2, 1, T, D) || !out_ok(qo, &ko, 1, -1, T, D)))
+    return PQKV_ERR_ARG;
+  p.q = q;
+  p.k = k;
+  p.qs = q_stride;
+  p.ks = k_stride;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.err = err_flag;
+  p.Hq = num_q_heads;
+  p.Hkv = num_kv_heads;
+  p.rows = num_q_heads + num_kv_heads;
+  const cudaError_t e =
+      launch_rope(dtype == PQKV_DTYPE_BF16, D, interleaved != 0, p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
+}
+
+int pqkv_qkv_norm_rope_write(const void* q, const void* k, const void* v, int dtype, int num_tokens,
+                             int num_q_heads, int num_kv_heads, int head_dim, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const float* q_weight, const float* k_weight, float eps,
+                             const int32_t* positions, int num_axes, const uint8_t* axis_of_pair,
+                             const float* cos_sin, int num_positions, int rot_dim, int interleaved, void* q_out,
+                             const int32_t* slot_mapping, void* cache, void* scales, void* outliers_idx,
+                             void* outliers_val, int kv_dtype, int num_blocks, int32_t* err_flag,
+                             pqkv_stream_t stream) {
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int T = num_tokens, D = head_dim;
+  if (rope_params(p.r, dtype, T, num_q_heads, D, q_weight, k_weight, eps, positions, num_axes, axis_of_pair, cos_sin,
+                  num_positions, rot_dim, interleaved) != PQKV_OK ||
+      num_kv_heads < 1 || num_kv_heads > 65535 || !rope_grid_ok(T, (int64_t)num_q_heads + 2 * (int64_t)num_kv_heads))
+    return PQKV_ERR_ARG;
+  if (!is_kv_dtype(kv_dtype) || (is_16(kv_dtype) && dtype != kv_dtype) || num_blocks < 1 ||
+      (int64_t)num_blocks * PQKV_BLOCK_SIZE > INT32_MAX)
+    return PQKV_ERR_ARG;
+  if (T == 0) return PQKV_OK;
+  const Heads in[3] = {{q, num_q_heads, q_stride}, {k, num_kv_heads, k_stride}, {v, num_kv_heads, v_stride}};
+  const Heads qo{q_out, num_q_heads, (int64_t)num_q_heads * D};
+  if (!err_flag || !slot_mapping || !cache || !aligned16(cache) || !heads_ok(in[0], D) || !heads_ok(in[1], D) ||
+      !heads_ok(in[2], D) || !heads_ok(qo, D) || !out_ok(qo, in, 3, 0, T, D))
+    return PQKV_ERR_ARG;
+  if (!is_16(kv_dtype) && (!scales || !aligned16(scales))) return PQKV_ERR_ARG;
+  if (kv_dtype == PQKV_DTYPE_FP4_E2M1 &&
+      (!outliers_idx || !outliers_val || !aligned16(outliers_idx) || !aligned16(outliers_val)))
+    return PQKV_ERR_ARG;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.qs = q_stride;
+  p.ks = k_stride;
+  p.vs = v_stride;
+  p.q_out = q_out;
+  p.slots = slot_mapping;
+  p.cache = static_cast<uint8_t*>(cache);
+  p.err = err_flag;
+  p.Hq = num_q_heads;
+  p.Hkv = num_kv_heads;
+  p.nb = num_blocks;
+  p.rows = is_16(kv_dtype) ? num_q_heads + 2 * num_kv_heads : num_q_heads;
+  cudaError_t e = launch_rope(dtype == PQKV_DTYPE_BF16, D, interleaved != 0, p, st);
+  if (e == cudaSuccess && !is_16(kv_dtype)) {
+    WriteParams w;
+    std::memset(&w, 0, sizeof(w));
+    w.k = k;
+    w.v = v;
+    w.slots = slot_mapping;
+    w.cache = static_cast<uint8_t*>(cache);
+    w.scales = static_cast<uint8_t*>(scales);
+    w.oidx = static_cast<uint8_t*>(outliers_idx);
+    w.oval = static_cast<uint8_t*>(outliers_val);
+    w.err = err_flag;
+    w.T = T;
+    w.nb = num_blocks;
+    w.Hkv = num_kv_heads;
+    w.rope = p.r;
+    w.ks = k_stride;
+    w.vs = v_stride;
+    e = launch_write_rope(kv_dtype, dtype, D, interleaved != 0, w, st);
+  }
   return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
 }
 

@@ -1,0 +1,171 @@
+// batch.cu -- block tables, slot mapping, positions and offsets of a batch,
+// from request lengths that are on the GPU.
+//
+// "vLLM" glossary, "PagedAttention" (logical to physical blocks) and
+// "Continuous batching" (every iteration has another batch): request b holds
+// s_b tokens and adds n_b. It needs ceil((s_b + n_b) / 16) - ceil(s_b / 16) new
+// blocks, the next ones of the step's flat id list; token s_b + i takes row
+// N_b + i of the batch (N, M: exclusive sums of new tokens and new blocks) and
+// slot 16 table_b[p / 16] + p % 16.
+//
+// One launch, no workspace: every CTA sums the lengths of all requests into
+// shared memory for itself (at most 4096 pairs, from L2), then the CTAs share
+// out the rows and the new blocks, a thread finding its request by bisection.
+// A row reads its block id from the id list, or from the one table entry that
+// holds the request's open block (which no thread writes), so no CTA waits for
+// another's table entries.
+#include "batch.cuh"
+
+namespace pqkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+__device__ __forceinline__ int blocks_of(int tokens) { return (tokens + kBlock - 1) / kBlock; }
+
+// Lengths of request i: its start and new tokens, zero new ones (and false) if
+// they are negative or do not fit a table row.
+__device__ __forceinline__ bool lengths(const BatchParams& p, int i, int& s, int& n) {
+  s = p.start[i];
+  n = p.num_new[i];
+  const bool ok = s >= 0 && n >= 0 && (long long)s + n <= (long long)kBlock * p.maxblk;
+  if (!ok) s = n = 0;
+  return ok;
+}
+
+// Largest b in [0, B) with cum[b] <= i, for cum[0] = 0 <= i < cum[B]: the
+// request that row (or new block) i belongs to.
+__device__ __forceinline__ int owner(const int* cum, int B, int i) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) build_batch_kernel(const BatchParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ int smem[];
+  int* tok = smem;            // [B + 1] first row of each request
+  int* blk = smem + p.B + 1;  // [B + 1] first new block of each request
+  __shared__ long long warp_tok[kThreads / 32], warp_blk[kThreads / 32];
+  __shared__ int total_tok, total_blk;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int lo = min(p.B, tid * per), hi = min(p.B, lo + per);
+
+  // sums in 64 bits: 4096 requests of up to 2^31 tokens
+  long long t = 0, m = 0;
+  for (int i = lo; i < hi; ++i) {
+    int s, n;
+    lengths(p, i, s, n);
+    t += n;
+    m += blocks_of(s + n) - blocks_of(s);
+  }
+  long long ti = t, mi = m;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(kFull, ti, o), b = __shfl_up_sync(kFull, mi, o);
+    if (lane >= o) {
+      ti += a;
+      mi += b;
+    }
+  }
+  if (lane == 31) {
+    warp_tok[warp] = ti;
+    warp_blk[warp] = mi;
+  }
+  if (tid == 0) {
+    total_tok = total_blk = 0;
+    tok[0] = blk[0] = 0;
+  }
+  __syncthreads();
+  t = ti - t;
+  m = mi - m;
+  for (int w = 0; w < warp; ++w) {
+    t += warp_tok[w];
+    m += warp_blk[w];
+  }
+  // Requests fit from the first one up to the one whose rows or blocks pass
+  // what there is; it and all behind it are left out whole (both sums only
+  // grow, so whether a request fits needs no other thread's answer).
+  int bits = 0;
+  for (int i = lo; i < hi; ++i) {
+    int s, n;
+    if (!lengths(p, i, s, n)) bits |= PQKV_DEVERR_SEQ_LEN;
+    t += n;
+    m += blocks_of(s + n) - blocks_of(s);
+    const bool fits = t <= p.cap && m <= p.n_ids;
+    if (!fits) bits |= PQKV_DEVERR_CAPACITY;
+    tok[i + 1] = fits ? (int)t : -1;
+    blk[i + 1] = fits ? (int)m : -1;
+    if (fits) {
+      atomicMax(&total_tok, (int)t);
+      atomicMax(&total_blk, (int)m);
+    }
+    if (blockIdx.x == 0) p.lens[i] = fits ? s + n : 0;
+  }
+  if (bits && blockIdx.x == 0) raise_flag(p.err, bits);
+  __syncthreads();
+  const int T = total_tok, M = total_blk;
+  for (int i = lo; i < hi; ++i) {
+    if (tok[i + 1] < 0) {
+      tok[i + 1] = T;
+      blk[i + 1] = M;
+    }
+    if (blockIdx.x == 0) p.cu[i + 1] = tok[i + 1];
+  }
+  if (blockIdx.x == 0 && tid == 0) p.cu[0] = 0;
+  __syncthreads();
+
+  const int step = gridDim.x * kThreads;
+  for (int i = blockIdx.x * kThreads + tid; i < M; i += step) {
+    const int b = owner(blk, p.B, i);
+    const int id = p.ids[i];
+    const bool ok = id >= 0 && id < p.nb;
+    if (!ok) raise_flag(p.err, PQKV_DEVERR_BLOCK_ID);
+    p.tables[(size_t)b * p.maxblk + blocks_of(p.start[b]) + (i - blk[b])] = ok ? id : -1;
+  }
+  for (long long i = (long long)blockIdx.x * kThreads + tid; i < p.cap; i += step) {
+    int slot = -1, pos = 0;
+    if (i < T) {
+      const int b = owner(tok, p.B, (int)i);
+      const int s = p.start[b];
+      pos = s + ((int)i - tok[b]);
+      const int j = pos / kBlock, have = blocks_of(s);
+      const int id = j < have ? p.tables[(size_t)b * p.maxblk + j] : p.ids[blk[b] + j - have];
+      if (id >= 0 && id < p.nb)
+        slot = id * kBlock + pos % kBlock;
+      else
+        raise_flag(p.err, PQKV_DEVERR_BLOCK_ID);
+    }
+    p.slots[i] = slot;
+    p.positions[i] = pos;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_build_batch(const BatchParams& p, int sms, cudaStream_t st) {
+  const long long items = p.cap > p.n_ids ? p.cap : p.n_ids;
+  const long long need = (items + kThreads - 1) / kThreads;
+  const int grid = (int)(need < 1 ? 1 : need < 4LL * sms ? need : 4LL * sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 2 * (size_t)(p.B + 1) * sizeof(int);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, build_batch_kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace pqkv

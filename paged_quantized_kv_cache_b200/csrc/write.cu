@@ -69,11 +69,51 @@ __device__ __forceinline__ int run_length(const WriteParams& p, int ts, int s0, 
   return __ffs(~m) - 1;  // bit 0 is always set
 }
 
+// Where a quantizing kernel takes its rows from: contiguous K and V, or rows of
+// a projection's output whose keys are normed and turned first (half-split or
+// interleaved pairs).
+enum { kSrcPlain = 0, kSrcRopeHalf = 1, kSrcRopeInterleaved = 2 };
+
+// The run's rows (tokens ts .. ts + n - 1 of KV head h, K or V) as 16-bit values
+// in this warp's shared rows: keys through norm_rotate and rounded, as
+// qk_norm_rope leaves them, values as they are.
+template <int D, bool BF16, int SRC>
+__device__ __forceinline__ void stage_run(const WriteParams& p, int ts, int n, int h, int kv, int lane,
+                                          uint16_t* rows) {
+  constexpr bool IL = SRC == kSrcRopeInterleaved;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const int i0 = 4 * (lane % kLanes);
+  int a, b;
+  pair_channels<D, IL>(i0, p.rope.rot, a, b);
+  const bool norm = kv == 0 && p.rope.k_weight != nullptr;
+  Pairs w = {};
+  if (norm) w = load_weight<IL>(p.rope.k_weight, a, b);
+  __syncwarp();  // the previous run's rows are read
+  for (int j0 = 0; j0 < n; j0 += kRows) {
+    const int j = j0 + lane / kLanes;
+    const bool mine = j < n;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (mine) {
+      const uint16_t* src = kv ? static_cast<const uint16_t*>(p.v) + (size_t)(ts + j) * p.vs
+                               : static_cast<const uint16_t*>(p.k) + (size_t)(ts + j) * p.ks;
+      raw = load_pairs<IL>(src + (size_t)h * D, a, b);
+    }
+    if (kv == 0) {
+      Pairs cs = {};
+      const bool ok = !mine || load_angles<D>(p.rope, ts + j, i0, cs);
+      const Pairs z = norm_rotate<D>(unpack_pairs<BF16, IL>(raw), norm, w, p.rope.eps, 2 * i0 < p.rope.rot, cs);
+      raw = ok ? pack_pairs<BF16, IL>(z) : make_uint4(0, 0, 0, 0);
+    }
+    if (mine) store_pairs<IL>(rows + j * D, a, b, raw);
+  }
+  __syncwarp();
+}
+
 }  // namespace
 
 // ---- 16-bit formats: one warp copies the K and V rows of one (token, head) ----
 template <int D>
-__global__ void __launch_bounds__(256) write16_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(256) write16_kernel(const __grid_constant__ WriteParams p) {
   // inputs may come from the previous kernel; let the next one start launching
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -97,12 +137,13 @@ __global__ void __launch_bounds__(256) write16_kernel(const WriteParams p) {
 }
 
 // ---- FP8: absmax scale per (block, head, K|V), grown on append ----
-template <int KVF, int D, bool INBF16>
-__global__ void __launch_bounds__(128) write_fp8_kernel(const WriteParams p) {
+template <int KVF, int D, bool INBF16, int SRC>
+__global__ void __launch_bounds__(128) write_fp8_kernel(const __grid_constant__ WriteParams p) {
   // inputs may come from the previous kernel; let the next one start launching
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int CPL = D / 32;  // channels per lane
+  __shared__ __align__(16) uint16_t s_rows[SRC == kSrcPlain ? 1 : 4][SRC == kSrcPlain ? 8 : kBlock * D];
   constexpr float kMax = (KVF == PQKV_DTYPE_FP8_E4M3) ? 448.0f : 57344.0f;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int win = blockIdx.x * 4 + warp;
@@ -119,13 +160,17 @@ __global__ void __launch_bounds__(128) write_fp8_kernel(const WriteParams p) {
     const size_t pair = (size_t)blk * p.Hkv + h;
     {
       const void* x = kv ? p.v : p.k;
+      if constexpr (SRC != kSrcPlain) stage_run<D, INBF16, SRC>(p, ts, n, h, kv, lane, s_rows[warp]);
       float xs[kBlock][CPL];
       float a = 0.f;
 #pragma unroll
       for (int j = 0; j < kBlock; ++j) {
 #pragma unroll
         for (int e = 0; e < CPL; ++e) {
-          xs[j][e] = (j < n) ? in_at<INBF16>(x, ((size_t)(ts + j) * p.Hkv + h) * D + lane * CPL + e) : 0.f;
+          if constexpr (SRC != kSrcPlain)
+            xs[j][e] = (j < n) ? in_at<INBF16>(s_rows[warp], j * D + lane * CPL + e) : 0.f;
+          else
+            xs[j][e] = (j < n) ? in_at<INBF16>(x, ((size_t)(ts + j) * p.Hkv + h) * D + lane * CPL + e) : 0.f;
           a = fmaxf(a, fabsf(xs[j][e]));
         }
       }
@@ -222,8 +267,8 @@ __device__ __forceinline__ uint2 e2m1_codes16(const float (&x)[16], float d, flo
 // rows of a V token pair (r, r ^ 1) sit in lanes l and l ^ GPL.
 // Four CTAs per SM (at most 128 registers a thread): the kernel is bound by
 // instruction issue, and 16 warps per SM hide more latency than 12.
-template <int D, bool INBF16>
-__global__ void __launch_bounds__(128, 4) write_fp4_kernel(const WriteParams p) {
+template <int D, bool INBF16, int SRC>
+__global__ void __launch_bounds__(128, 4) write_fp4_kernel(const __grid_constant__ WriteParams p) {
   // inputs may come from the previous kernel; let the next one start launching
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -233,6 +278,7 @@ __global__ void __launch_bounds__(128, 4) write_fp4_kernel(const WriteParams p) 
   constexpr int PREC = INBF16 ? 8 : 11;  // significant bits of an input value
   __shared__ float s_norm[4][D];
   __shared__ int s_oc[4][kOutSlots];
+  __shared__ __align__(16) uint16_t s_rows[SRC == kSrcPlain ? 1 : 4][SRC == kSrcPlain ? 8 : kBlock * D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane % GPL, tl = lane / GPL;
   const int win = blockIdx.x * 4 + warp;
@@ -248,6 +294,7 @@ __global__ void __launch_bounds__(128, 4) write_fp4_kernel(const WriteParams p) 
     const int blk = s0 >> 4, off0 = s0 & 15;
     const size_t tile = ((size_t)blk * p.Hkv + h) * 2 + kv;  // (block, head, K|V) index
     const auto* x = reinterpret_cast<const uint16_t*>(kv ? p.v : p.k);
+    if constexpr (SRC != kSrcPlain) stage_run<D, INBF16, SRC>(p, ts, n, h, kv, lane, s_rows[warp]);
     // this lane's rows of the run (rows outside it read as zeros)
     float xs[TPL][16];
 #pragma unroll
@@ -255,9 +302,15 @@ __global__ void __launch_bounds__(128, 4) write_fp4_kernel(const WriteParams p) 
       const int r = tl + TL * i, j = r - off0;
       uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
       if (j >= 0 && j < n) {
-        const uint4* src = reinterpret_cast<const uint4*>(x + ((size_t)(ts + j) * p.Hkv + h) * D + kGroup * g);
-        u0 = __ldg(src);
-        u1 = __ldg(src + 1);
+        if constexpr (SRC != kSrcPlain) {
+          const uint4* src = reinterpret_cast<const uint4*>(s_rows[warp] + j * D + kGroup * g);
+          u0 = src[0];
+          u1 = src[1];
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(x + ((size_t)(ts + j) * p.Hkv + h) * D + kGroup * g);
+          u0 = __ldg(src);
+          u1 = __ldg(src + 1);
+        }
       }
       const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
@@ -428,7 +481,8 @@ __global__ void __launch_bounds__(128, 4) write_fp4_kernel(const WriteParams p) 
           if (k == slot) c = oc[k];
         unsigned short hv = 0;
         if (c < D) {
-          const uint16_t raw = x[((size_t)(ts + j) * p.Hkv + h) * D + c];
+          const uint16_t raw =
+              SRC != kSrcPlain ? s_rows[warp][j * D + c] : x[((size_t)(ts + j) * p.Hkv + h) * D + c];
           hv = INBF16 ? __half_as_ushort(__float2half_rn(__uint_as_float((uint32_t)raw << 16))) : raw;
         }
         reinterpret_cast<unsigned short*>(p.oval)[(tile * kBlock + r) * kOutSlots + slot] = hv;
@@ -536,21 +590,15 @@ static cudaError_t launch_pdl(void (*kern)(Args...), dim3 grid, unsigned block, 
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-cudaError_t launch_write(int kv_dtype, int in_dtype, int D, const WriteParams& p, cudaStream_t st) {
-  if (p.T <= 0) return cudaSuccess;
-  const bool bf = (in_dtype == PQKV_DTYPE_BF16);
-  if (kv_dtype == PQKV_DTYPE_FP16 || kv_dtype == PQKV_DTYPE_BF16) {
-    const long warps = (long)p.T * p.Hkv;
-    const int grid = (int)((warps + 7) / 8);
-    return D == 128 ? launch_pdl(write16_kernel<128>, dim3(grid), 256, st, p)
-                    : launch_pdl(write16_kernel<64>, dim3(grid), 256, st, p);
-  }
+// SRC other than kSrcPlain: quantized formats only.
+template <int SRC>
+static cudaError_t launch_write_src(int kv_dtype, bool bf, int D, const WriteParams& p, cudaStream_t st) {
   // a warp owns the runs starting in a window of tpw tokens of one (head, K|V)
   WriteParams q = p;
   q.tpw = (p.T <= 8192) ? 1 : 32;
   const dim3 grid((unsigned)((p.T + 4 * q.tpw - 1) / (4 * q.tpw)), (unsigned)p.Hkv, 2u);
 #define PQKV_W8(F, DD, B) \
-  if (kv_dtype == F && D == DD && bf == B) return launch_pdl(write_fp8_kernel<F, DD, B>, grid, 128, st, q);
+  if (kv_dtype == F && D == DD && bf == B) return launch_pdl(write_fp8_kernel<F, DD, B, SRC>, grid, 128, st, q);
   PQKV_W8(PQKV_DTYPE_FP8_E4M3, 128, true)
   PQKV_W8(PQKV_DTYPE_FP8_E4M3, 128, false)
   PQKV_W8(PQKV_DTYPE_FP8_E4M3, 64, true)
@@ -562,12 +610,31 @@ cudaError_t launch_write(int kv_dtype, int in_dtype, int D, const WriteParams& p
 #undef PQKV_W8
   if (kv_dtype == PQKV_DTYPE_FP4_E2M1) {
     if (D == 128)
-      return bf ? launch_pdl(write_fp4_kernel<128, true>, grid, 128, st, q)
-                : launch_pdl(write_fp4_kernel<128, false>, grid, 128, st, q);
-    return bf ? launch_pdl(write_fp4_kernel<64, true>, grid, 128, st, q)
-              : launch_pdl(write_fp4_kernel<64, false>, grid, 128, st, q);
+      return bf ? launch_pdl(write_fp4_kernel<128, true, SRC>, grid, 128, st, q)
+                : launch_pdl(write_fp4_kernel<128, false, SRC>, grid, 128, st, q);
+    return bf ? launch_pdl(write_fp4_kernel<64, true, SRC>, grid, 128, st, q)
+              : launch_pdl(write_fp4_kernel<64, false, SRC>, grid, 128, st, q);
   }
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_write(int kv_dtype, int in_dtype, int D, const WriteParams& p, cudaStream_t st) {
+  if (p.T <= 0) return cudaSuccess;
+  if (kv_dtype == PQKV_DTYPE_FP16 || kv_dtype == PQKV_DTYPE_BF16) {
+    const long warps = (long)p.T * p.Hkv;
+    const int grid = (int)((warps + 7) / 8);
+    return D == 128 ? launch_pdl(write16_kernel<128>, dim3(grid), 256, st, p)
+                    : launch_pdl(write16_kernel<64>, dim3(grid), 256, st, p);
+  }
+  return launch_write_src<kSrcPlain>(kv_dtype, in_dtype == PQKV_DTYPE_BF16, D, p, st);
+}
+
+cudaError_t launch_write_rope(int kv_dtype, int in_dtype, int D, bool interleaved, const WriteParams& p,
+                              cudaStream_t st) {
+  if (p.T <= 0) return cudaSuccess;
+  const bool bf = in_dtype == PQKV_DTYPE_BF16;
+  return interleaved ? launch_write_src<kSrcRopeInterleaved>(kv_dtype, bf, D, p, st)
+                     : launch_write_src<kSrcRopeHalf>(kv_dtype, bf, D, p, st);
 }
 
 cudaError_t launch_encode(int code_dtype, const float* x, int64_t n, uint8_t* out, cudaStream_t st) {

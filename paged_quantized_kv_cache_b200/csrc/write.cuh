@@ -1,7 +1,7 @@
 // write.cuh -- parameters and launchers of the cache-write and encode kernels.
 #pragma once
 
-#include "common.cuh"
+#include "rope.cuh"
 
 namespace pqkv {
 
@@ -16,9 +16,16 @@ struct WriteParams {
   int32_t* err;
   int T, nb, Hkv;
   int tpw;  // tokens per warp window (set by the launcher)
+  // keys normed and turned on the way (launch_write_rope): k and v are then
+  // rows of ks / vs elements per token
+  RowParams rope;
+  long long ks, vs;
 };
 
 cudaError_t launch_write(int kv_dtype, int in_dtype, int D, const WriteParams& p, cudaStream_t st);
+// Quantized formats, keys taken through norm_rotate (p.rope) first.
+cudaError_t launch_write_rope(int kv_dtype, int in_dtype, int D, bool interleaved, const WriteParams& p,
+                              cudaStream_t st);
 cudaError_t launch_encode(int code_dtype, const float* x, int64_t n, uint8_t* out, cudaStream_t st);
 
 }  // namespace pqkv
