@@ -321,39 +321,43 @@ def paged_prefill_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len:
     _check("pqkv_paged_prefill_attention", st)
 
 
-class _OnDevice:
-    """Pointers of a call's tensors, all on one device, which is current while the library is called."""
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """Index of the device that a call's tensors are on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.get_device()
 
-    def __init__(self, t: torch.Tensor, name: str):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-        self.index = t.get_device()
 
-    def ptr(self, t: Optional[torch.Tensor], name: str, dtype: Optional[torch.dtype] = None,
-            contiguous: bool = True) -> Optional[int]:
-        if t is None:
-            return None
-        if not isinstance(t, torch.Tensor) or t.get_device() != self.index:
-            raise ValueError("%s must be a tensor on cuda:%d" % (name, self.index))
-        if dtype is not None and t.dtype != dtype:
-            raise ValueError("%s must be %s" % (name, dtype))
-        if contiguous and not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        return t.data_ptr()
+def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, device: int, contiguous: bool = True) -> int:
+    """Pointer of a tensor of `dtype` on `device`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise ValueError("%s must be a tensor on cuda:%d" % (name, device))
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s" % (name, dtype))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
-    def cache(self, c: KVCache):
-        return (self.ptr(c.cache, "cache"), self.ptr(c.scales, "scales"), self.ptr(c.outliers_idx, "outliers_idx"),
-                self.ptr(c.outliers_val, "outliers_val"))
 
-    def call(self, func: str, stream, *args) -> None:
-        if stream is None:
-            stream = torch.cuda.current_stream(self.index)
-        if torch.cuda.current_device() == self.index:
-            st = getattr(lib(), func)(*args, stream.cuda_stream)
-        else:
-            with torch.cuda.device(self.index):
-                st = getattr(lib(), func)(*args, stream.cuda_stream)
-        _check(func, st)
+def _cache_args(c: KVCache, device: int):
+    u8 = torch.uint8
+    return (_arg(c.cache, "cache", u8, device),
+            None if c.scales is None else _arg(c.scales, "scales", u8, device),
+            None if c.outliers_idx is None else _arg(c.outliers_idx, "outliers_idx", u8, device),
+            None if c.outliers_val is None else _arg(c.outliers_val, "outliers_val", u8, device))
+
+
+def _call(func: str, device: int, stream, *args) -> None:
+    """The library's function on `stream` (None: the device's current one), with the device current."""
+    f = getattr(_lib_handle or lib(), func)
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        st = f(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, handle)
+    if st != OK:
+        raise PqkvError(func, st)
 
 
 def paged_cross_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: int, cache: KVCache,
@@ -361,25 +365,25 @@ def paged_cross_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: i
                           err_flag: torch.Tensor, kv_ranges: Optional[torch.Tensor] = None, stream=None) -> None:
     """pqkv_paged_cross_attention: q, out [T][Hq][D]; cu_q_lens int32 [B + 1]; block_tables int32
     [B][max_blocks] and kv_lens int32 [B] of the encoder's states; kv_ranges int32 [T][2] or None."""
-    dev = _OnDevice(q, "q")
-    i32 = torch.int32
-    T, Hq, D = q.shape
-    B = kv_lens.numel()
-    if out.shape != q.shape or D != cache.head_dim:
-        raise ValueError("out must match q, and q the cache's head_dim")
+    dev, i32, dtype = _device_of(q, "q"), torch.int32, q.dtype
+    shape = q.shape
+    B, table = kv_lens.numel(), block_tables.shape
+    if len(shape) != 3 or out.shape != shape or shape[2] != cache.head_dim:
+        raise ValueError("q must be [T][num_q_heads][head_dim] of the cache's head_dim, and out match it")
     if cu_q_lens.numel() != B + 1:
         raise ValueError("cu_q_lens must be int32 [B + 1]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+    if len(table) != 2 or table[0] != B:
         raise ValueError("block_tables must be int32 [B][max_blocks_per_seq]")
-    if kv_ranges is not None and kv_ranges.shape != (T, 2):
+    if kv_ranges is not None and kv_ranges.shape != (shape[0], 2):
         raise ValueError("kv_ranges must be int32 [T][2]")
-    if T == 0:
+    if shape[0] == 0:
         return
-    dev.call("pqkv_paged_cross_attention", stream, dev.ptr(q, "q"), _dt_of(q, "q"), B, max_q_len, Hq,
-             dev.ptr(cu_q_lens, "cu_q_lens", i32), *dev.cache(cache), cache.kv_dtype, cache.num_blocks,
-             cache.num_kv_heads, D, dev.ptr(block_tables, "block_tables", i32), block_tables.shape[1],
-             dev.ptr(kv_lens, "kv_lens", i32), dev.ptr(kv_ranges, "kv_ranges", i32), scale,
-             dev.ptr(out, "out", q.dtype), dev.ptr(err_flag, "err_flag", i32))
+    _call("pqkv_paged_cross_attention", dev, stream, _arg(q, "q", dtype, dev), _dt_of(q, "q"), B, max_q_len, shape[1],
+          _arg(cu_q_lens, "cu_q_lens", i32, dev), *_cache_args(cache, dev), cache.kv_dtype, cache.num_blocks,
+          cache.num_kv_heads, shape[2], _arg(block_tables, "block_tables", i32, dev), table[1],
+          _arg(kv_lens, "kv_lens", i32, dev),
+          None if kv_ranges is None else _arg(kv_ranges, "kv_ranges", i32, dev), scale,
+          _arg(out, "out", dtype, dev), _arg(err_flag, "err_flag", i32, dev))
 
 
 def build_batch(start_pos: torch.Tensor, num_new: torch.Tensor, new_block_ids: torch.Tensor,
@@ -388,21 +392,20 @@ def build_batch(start_pos: torch.Tensor, num_new: torch.Tensor, new_block_ids: t
     """pqkv_build_batch: start_pos, num_new int32 [B] and new_block_ids int32 [n] on the device -> block_tables
     int32 [B][max_blocks] (in place), slot_mapping and positions int32 [max_tokens], cu_q_lens int32 [B + 1],
     seq_lens int32 [B]."""
-    dev = _OnDevice(start_pos, "start_pos")
-    i32 = torch.int32
-    B = start_pos.numel()
+    dev, i32 = _device_of(start_pos, "start_pos"), torch.int32
+    B, capacity, table = start_pos.numel(), slot_mapping.numel(), block_tables.shape
     if num_new.numel() != B or seq_lens.numel() != B or cu_q_lens.numel() != B + 1:
         raise ValueError("num_new and seq_lens must be [B], cu_q_lens [B + 1]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+    if len(table) != 2 or table[0] != B:
         raise ValueError("block_tables must be int32 [B][max_blocks_per_seq]")
-    if positions.numel() != slot_mapping.numel():
+    if positions.numel() != capacity:
         raise ValueError("positions and slot_mapping must be of one size")
-    dev.call("pqkv_build_batch", stream, dev.ptr(start_pos, "start_pos", i32), dev.ptr(num_new, "num_new", i32), B,
-             dev.ptr(new_block_ids, "new_block_ids", i32), new_block_ids.numel(),
-             dev.ptr(block_tables, "block_tables", i32), block_tables.shape[1], num_blocks, slot_mapping.numel(),
-             dev.ptr(slot_mapping, "slot_mapping", i32), dev.ptr(positions, "positions", i32),
-             dev.ptr(cu_q_lens, "cu_q_lens", i32), dev.ptr(seq_lens, "seq_lens", i32),
-             dev.ptr(err_flag, "err_flag", i32))
+    _call("pqkv_build_batch", dev, stream, _arg(start_pos, "start_pos", i32, dev), _arg(num_new, "num_new", i32, dev), B,
+          _arg(new_block_ids, "new_block_ids", i32, dev), new_block_ids.numel(),
+          _arg(block_tables, "block_tables", i32, dev), table[1], num_blocks, capacity,
+          _arg(slot_mapping, "slot_mapping", i32, dev), _arg(positions, "positions", i32, dev),
+          _arg(cu_q_lens, "cu_q_lens", i32, dev), _arg(seq_lens, "seq_lens", i32, dev),
+          _arg(err_flag, "err_flag", i32, dev))
 
 
 @dataclasses.dataclass
@@ -415,38 +418,39 @@ class Rotary:
     interleaved: bool = False
 
 
-def _heads(dev: _OnDevice, x: torch.Tensor, name: str, T: int, D: int, dtype: torch.dtype) -> Tuple[int, int]:
-    """Pointer and token stride of [T][H][D] rows whose heads are contiguous within a token."""
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.stride(2) != 1 or \
-            (x.stride(1) != D and x.shape[1] > 1):
+def _heads(x: torch.Tensor, name: str, T: int, D: int, dtype: torch.dtype, device: int) -> Tuple[int, int, int]:
+    """Pointer, heads and token stride of [T][H][D] rows whose heads are contiguous within a token."""
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or stride[2] != 1 or (stride[1] != D and shape[1] > 1):
         raise ValueError("%s must be [T][heads][head_dim] with contiguous heads" % name)
     # the stride of a dimension of one token means nothing
-    return dev.ptr(x, name, dtype, contiguous=False), (x.stride(0) if T > 1 else x.shape[1] * D)
+    return _arg(x, name, dtype, device, False), shape[1], stride[0] if T > 1 else shape[1] * D
 
 
-def _rotary_args(dev: _OnDevice, rotary: Optional[Rotary], positions: Optional[torch.Tensor], T: int):
+def _rotary_args(rotary: Optional[Rotary], positions: Optional[torch.Tensor], T: int, device: int):
     """positions, num_axes, axis_of_pair, cos_sin, num_positions, rot_dim, interleaved."""
     if rotary is None:
         return None, 0, None, None, 0, 0, 0
-    table = rotary.cos_sin
-    if table.dim() != 2:
+    table, axis = rotary.cos_sin, rotary.axis_of_pair
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("cos_sin must be float32 [num_positions][rot_dim]")
-    rot = table.shape[1]
-    if rotary.axis_of_pair and len(rotary.axis_of_pair) != rot // 2:
+    if shape[1] == 0:
+        return None, 0, None, None, 0, 0, 0
+    if axis and len(axis) != shape[1] // 2:
         raise ValueError("axis_of_pair must hold rot_dim / 2 bytes")
-    axes = 1
-    if rot:
-        if positions is None or positions.dim() not in (1, 2) or positions.shape[-1] != T:
-            raise ValueError("positions must be int32 [T] or [axes][T]")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-    return (dev.ptr(positions, "positions", torch.int32), axes, rotary.axis_of_pair or None,
-            dev.ptr(table, "cos_sin", torch.float32), table.shape[0], rot, int(rotary.interleaved))
+    if positions is None or len(positions.shape) not in (1, 2) or positions.shape[-1] != T:
+        raise ValueError("positions must be int32 [T] or [axes][T]")
+    return (_arg(positions, "positions", torch.int32, device), positions.numel() // max(1, T), axis or None,
+            _arg(table, "cos_sin", torch.float32, device), shape[0], shape[1], 1 if rotary.interleaved else 0)
 
 
-def _weight(dev: _OnDevice, w: Optional[torch.Tensor], name: str, D: int) -> Optional[int]:
-    if w is not None and w.numel() != D:
+def _weight(w: Optional[torch.Tensor], name: str, D: int, device: int) -> Optional[int]:
+    if w is None:
+        return None
+    if w.numel() != D:
         raise ValueError("%s must be float32 [head_dim]" % name)
-    return dev.ptr(w, name, torch.float32)
+    return _arg(w, name, torch.float32, device)
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -456,19 +460,20 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     """pqkv_qk_norm_rope: q [T][Hq][D] and k [T][Hkv][D] (or None), the heads of a token contiguous, any stride
     from one token to the next; positions int32 [T] or [axes][T]; q_out, k_out contiguous, or the input itself.
     A weight of None leaves the norm out, a rotary of None the rotation."""
-    dev = _OnDevice(q, "q")
+    dev, dtype = _device_of(q, "q"), q.dtype
     if q.dim() != 3:
         raise ValueError("q must be [T][num_q_heads][head_dim]")
-    T, Hq, D = q.shape
-    dt = _dt_of(q, "q")
+    T, _, D = q.shape
+    if T == 0:
+        return
     if q_out.shape != q.shape or (k is None) != (k_out is None) or (k is not None and k_out.shape != k.shape):
         raise ValueError("q_out and k_out must match q and k")
-    qp, qs = _heads(dev, q, "q", T, D, q.dtype)
-    kp, ks = _heads(dev, k, "k", T, D, q.dtype) if k is not None else (None, 0)
-    dev.call("pqkv_qk_norm_rope", stream, qp, kp, dt, T, Hq, k.shape[1] if k is not None else 0, D, qs, ks,
-             _weight(dev, q_weight, "q_weight", D), _weight(dev, k_weight, "k_weight", D), eps,
-             *_rotary_args(dev, rotary, positions, T), dev.ptr(q_out, "q_out", q.dtype),
-             dev.ptr(k_out, "k_out", q.dtype), dev.ptr(err_flag, "err_flag", torch.int32))
+    qp, Hq, qs = _heads(q, "q", T, D, dtype, dev)
+    kp, Hkv, ks = (None, 0, 0) if k is None else _heads(k, "k", T, D, dtype, dev)
+    _call("pqkv_qk_norm_rope", dev, stream, qp, kp, _dt_of(q, "q"), T, Hq, Hkv, D, qs, ks,
+          _weight(q_weight, "q_weight", D, dev), _weight(k_weight, "k_weight", D, dev), eps,
+          *_rotary_args(rotary, positions, T, dev), _arg(q_out, "q_out", dtype, dev),
+          None if k is None else _arg(k_out, "k_out", dtype, dev), _arg(err_flag, "err_flag", torch.int32, dev))
 
 
 def qkv_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
@@ -477,25 +482,26 @@ def qkv_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, posit
                         k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
     """pqkv_qkv_norm_rope_write: qk_norm_rope whose keys, with the values v [T][Hkv][D], go to the cache slots
     of slot_mapping int32 [T] as kv_cache_write would store them."""
-    dev = _OnDevice(q, "q")
+    dev, dtype, i32 = _device_of(q, "q"), q.dtype, torch.int32
     if q.dim() != 3:
         raise ValueError("q must be [T][num_q_heads][head_dim]")
-    T, Hq, D = q.shape
-    dt = _dt_of(q, "q")
+    T, _, D = q.shape
+    if T == 0:
+        return
     if q_out.shape != q.shape:
         raise ValueError("q_out must match q")
-    if k.shape != (T, cache.num_kv_heads, cache.head_dim) or v.shape != k.shape or D != cache.head_dim:
+    qp, Hq, qs = _heads(q, "q", T, D, dtype, dev)
+    kp, Hkv, ks = _heads(k, "k", T, D, dtype, dev)
+    vp, Hv, vs = _heads(v, "v", T, D, dtype, dev)
+    if Hkv != cache.num_kv_heads or Hv != Hkv or D != cache.head_dim:
         raise ValueError("k and v must be [T][num_kv_heads][head_dim]")
     if slot_mapping.numel() != T:
         raise ValueError("slot_mapping must be int32 [T]")
-    qp, qs = _heads(dev, q, "q", T, D, q.dtype)
-    kp, ks = _heads(dev, k, "k", T, D, q.dtype)
-    vp, vs = _heads(dev, v, "v", T, D, q.dtype)
-    dev.call("pqkv_qkv_norm_rope_write", stream, qp, kp, vp, dt, T, Hq, k.shape[1], D, qs, ks, vs,
-             _weight(dev, q_weight, "q_weight", D), _weight(dev, k_weight, "k_weight", D), eps,
-             *_rotary_args(dev, rotary, positions, T), dev.ptr(q_out, "q_out", q.dtype),
-             dev.ptr(slot_mapping, "slot_mapping", torch.int32), *dev.cache(cache), cache.kv_dtype,
-             cache.num_blocks, dev.ptr(err_flag, "err_flag", torch.int32))
+    _call("pqkv_qkv_norm_rope_write", dev, stream, qp, kp, vp, _dt_of(q, "q"), T, Hq, Hkv, D, qs, ks, vs,
+          _weight(q_weight, "q_weight", D, dev), _weight(k_weight, "k_weight", D, dev), eps,
+          *_rotary_args(rotary, positions, T, dev), _arg(q_out, "q_out", dtype, dev),
+          _arg(slot_mapping, "slot_mapping", i32, dev), *_cache_args(cache, dev), cache.kv_dtype, cache.num_blocks,
+          _arg(err_flag, "err_flag", i32, dev))
 
 
 def encode(x: torch.Tensor, code_dtype: int, out: torch.Tensor, stream=None) -> None:

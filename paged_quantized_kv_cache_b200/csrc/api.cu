@@ -519,9 +519,14 @@ static int prefill_impl(bool cross, const void* q, int q_dtype, int batch, int m
   DeviceInfo di;
   if (!device_info(di)) return PQKV_ERR_CUDA;
   if ((size_t)di.max_smem < prefill_smem_bytes(kv_dtype, head_dim)) return PQKV_ERR_CUDA;
+  const bool few = cross && (int64_t)max_q_len * G <= kFewColumns;
+  // TMA row coordinates and grids fit 32 bits
+  if ((few || is_16(kv_dtype)) && (int64_t)num_blocks * num_kv_heads * 32 >= INT32_MAX) return PQKV_ERR_ARG;
+  if (cross && (int64_t)batch * num_kv_heads >= INT32_MAX / 16) return PQKV_ERR_ARG;
   CUtensorMap tmap;
   std::memset(&tmap, 0, sizeof(tmap));
-  if (is_16(kv_dtype) && !make_prefill_map(&tmap, cache, kv_dtype, num_blocks, num_kv_heads, head_dim))
+  if (few && !cached_cache_map(&tmap, cache, kv_dtype, num_blocks, num_kv_heads, head_dim)) return PQKV_ERR_CUDA;
+  if (!few && is_16(kv_dtype) && !make_prefill_map(&tmap, cache, kv_dtype, num_blocks, num_kv_heads, head_dim))
     return PQKV_ERR_CUDA;
   PrefillParams p;
   p.q = q;
@@ -545,20 +550,22 @@ static int prefill_impl(bool cross, const void* q, int q_dtype, int batch, int m
   p.timeout_ns = g_decode_wait_ns.load();
   p.drain_ns = kWaitLimitNs;
   p.ranges = ranges;
+  p.max_q = max_q_len;
   p.splits = 1;
   p.q_and = 0xFFFFFFFFu;
   p.q_xor = 0;
-  if (cross && scale < 0.f) {
+  if (cross && !few && scale < 0.f) {
     p.q_xor = 0x80008000u;
     p.scale_log2 = -p.scale_log2;
-  } else if (cross && scale == 0.f) {
+  } else if (cross && !few && scale == 0.f) {
     p.q_and = 0;
     p.scale_log2 = 1.f;
   }
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool q_bf16 = q_dtype == PQKV_DTYPE_BF16;
-  const cudaError_t e = cross ? launch_cross(kv_dtype, head_dim, q_bf16, tmap, p, di.sms, st)
-                              : launch_prefill(kv_dtype, head_dim, q_bf16, tmap, p, st);
+  const cudaError_t e = few     ? launch_cross_few(kv_dtype, head_dim, q_bf16, tmap, p, di.sms, st)
+                        : cross ? launch_cross(kv_dtype, head_dim, q_bf16, tmap, p, di.sms, st)
+                                : launch_prefill(kv_dtype, head_dim, q_bf16, tmap, p, st);
   return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
 }
 

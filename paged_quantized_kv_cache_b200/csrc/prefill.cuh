@@ -28,6 +28,7 @@ struct PrefillParams {
   uint64_t drain_ns;            // after giving up: limit of the wait for work still in flight
   // attention to an encoder's states only
   const int32_t* ranges;        // [cu_q[B]][2] positions each query token sees, or null: all
+  int max_q;                    // query tokens of the longest sequence
   int splits;                   // CTAs of a cluster that share a tile pair's KV range
   // The softmax takes a scale above 0 (masked scores are -inf before they are
   // scaled): a scale below 0 turns the sign of the queries' words instead, and
@@ -37,9 +38,14 @@ struct PrefillParams {
 
 cudaError_t launch_prefill(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap16, const PrefillParams& p,
                            cudaStream_t st);
-// Attention to an encoder's states (cross.cu); p.splits is set by the launcher.
+// Attention to an encoder's states: tiles of query rows on tcgen05 (cross.cu,
+// map as the prefill's), or at most kFewColumns rows per KV head (cross_few.cu,
+// map as the decode's; any sign of scale_log2). The launchers set p.splits.
+constexpr int kFewColumns = 16;
 cudaError_t launch_cross(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap16, const PrefillParams& p, int sms,
                          cudaStream_t st);
+cudaError_t launch_cross_few(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap, const PrefillParams& p,
+                             int sms, cudaStream_t st);
 size_t prefill_smem_bytes(int kv_dtype, int D);
 
 }  // namespace pqkv

@@ -139,6 +139,64 @@ def test_every_split_of_the_states(case, splits):
     _check(g, o, q, cu, bt, lens, 0.1, r)
 
 
+FEW = [
+    # query tokens a sequence; batch (8 KV heads: the states in 16, 8, 4, 2 and 1 parts)
+    ([1], "one of 16 parts"), ([2, 1], "8 parts"), ([4, 0, 3, 1], "4 parts"), ([1, 2] * 4, "2 parts"), ([2] * 20, "1 part"),
+]
+
+
+@pytest.mark.parametrize("qlens", [f[0] for f in FEW], ids=[f[1] for f in FEW])
+@pytest.mark.parametrize("case", CASES, ids=ID)
+def test_a_few_tokens(case, qlens):
+    """Up to 16 query rows per KV head, whole states and ranges (some without a position, some parts without a block)."""
+    G = case[3] // case[4]
+    qlens = [min(n, 16 // G) for n in qlens]
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(1, 1200, len(qlens))]
+    g, o, bt, cu, q, lens = _build(case, lens, qlens, seed=700 + len(qlens), wide=20)
+    _check(g, o, q, cu, bt, lens, 1 / np.sqrt(case[2]))
+    _check(g, o, q, cu, bt, lens, 1 / np.sqrt(case[2]), _ranges(rng, cu, lens))
+
+
+def test_few_tokens_edges():
+    for case in (CASES[0], CASES[5], CASES[6]):
+        g, o, bt, cu, q, lens = _build(case, [100, 0, 40, 260, 17], [1, 2, 0, 2, 1], seed=607)
+        out = _check(g, o, q, cu, bt, lens, 0.1)
+        assert (out[1:3] == 0).all()
+        for scale in (0.0, -0.4, 15.0):
+            _check(g, o, q, cu, bt, lens, scale)
+        bt[0, 1], bt[3, 4], bt[3, 16] = g.num_blocks, -1, 2 ** 31 - 1
+        _check(g, o, q, cu, bt, lens, 0.1, bits=pq.DEVERR_BLOCK_ID)
+        lens[0], lens[4] = -3, 16 * bt.shape[1] + 1
+        out = _check(g, o, q, cu, bt, lens, 0.1, bits=pq.DEVERR_BLOCK_ID | pq.DEVERR_SEQ_LEN)
+        assert (out[0] == 0).all() and (out[-1] == 0).all()
+        lens[0], lens[4] = 100, 17
+        out, err = _run(g, q, cu, bt, lens, 0.1, max_q_len=1)  # the second tokens are not computed
+        assert err == pq.DEVERR_BLOCK_ID | pq.DEVERR_SEQ_LEN and torch.isnan(out[2]).all() and not torch.isnan(out[3]).any()
+
+
+# 1500 positions in 16 parts: every copy is issued at the start and may land before the first wait; 12 sequences of
+# 3000: with 16-bit states the copies are what a warp waits for, and its waits run out; quantized states may be there
+# (in L2) before the warp is done with the blocks before them
+@pytest.mark.parametrize("lens", [[1500], [3000] * 12], ids=["short", "long"])
+@pytest.mark.parametrize("case", [CASES[0], CASES[4], CASES[6]], ids=ID)
+def test_few_tokens_wait_limit_runs_out_and_the_next_call_is_correct(case, lens):
+    g, o, bt, cu, q, lens = _build(case, lens, [1] * len(lens), seed=608)
+    seen = 0
+    pq.set_decode_wait_limit_ns(1)
+    try:
+        for _ in range(5):
+            _, e = _run(g, q, cu, bt, lens, 0.088)
+            assert e & ~pq.DEVERR_TIMEOUT == 0
+            seen += (e & pq.DEVERR_TIMEOUT) != 0
+            if seen:
+                break
+    finally:
+        pq.set_decode_wait_limit_ns(0)
+    assert seen or len(lens) == 1 or case[0] != pq.BF16
+    _check(g, o, q, cu, bt, lens, 0.088)
+
+
 def test_empty_and_rejected_sequences():
     case = CASES[1]
     lens, qlens = [40, 0, 30, 0, 20], [5, 4, 0, 1, 3]
