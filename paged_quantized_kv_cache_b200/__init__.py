@@ -3,7 +3,9 @@
 Argument marshalling only: every step runs in libpqkv.so (CUDA kernels for
 sm_100a and a C++ block pool) through its C ABI (include/pqkv.h). PyTorch is
 used for device memory and streams. If the library is missing this module
-raises at import; there is no other code path.
+raises at import; there is no other code path. The calls around a serving step
+(build_batch, qk_norm_rope, qkv_norm_rope_write, paged_cross_attention) go through
+_binding.so (csrc/python/binding.cpp), which does their marshalling in C++.
 
 Build the library with ``python -m paged_quantized_kv_cache_b200.build``; the
 first call into this module loads it and raises ImportError if it is missing.
@@ -115,6 +117,23 @@ def lib() -> ctypes.CDLL:
     if _lib_handle is None:
         _lib_handle = _load()
     return _lib_handle
+
+
+_binding_module = None
+
+
+def _load_binding():
+    """The loaded _binding.so, which holds the addresses of libpqkv.so's functions (loaded on first use)."""
+    global _binding_module
+    try:
+        from . import _binding as module
+    except ImportError as e:
+        raise ImportError("_binding.so is missing or does not load (run: python -m paged_quantized_kv_cache_b200.build): "
+                          "%s" % e) from e
+    module.bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
+        "pqkv_build_batch", "pqkv_qk_norm_rope", "pqkv_qkv_norm_rope_write", "pqkv_paged_cross_attention")))
+    _binding_module = module
+    return module
 
 
 class _LazyLib:
@@ -321,43 +340,21 @@ def paged_prefill_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len:
     _check("pqkv_paged_prefill_attention", st)
 
 
-def _device_of(t: torch.Tensor, name: str) -> int:
-    """Index of the device that a call's tensors are on."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    return t.get_device()
-
-
-def _arg(t: torch.Tensor, name: str, dtype: torch.dtype, device: int, contiguous: bool = True) -> int:
-    """Pointer of a tensor of `dtype` on `device`."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device:
-        raise ValueError("%s must be a tensor on cuda:%d" % (name, device))
-    if t.dtype is not dtype:
-        raise ValueError("%s must be %s" % (name, dtype))
-    if contiguous and not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
-
-
-def _cache_args(c: KVCache, device: int):
-    u8 = torch.uint8
-    return (_arg(c.cache, "cache", u8, device),
-            None if c.scales is None else _arg(c.scales, "scales", u8, device),
-            None if c.outliers_idx is None else _arg(c.outliers_idx, "outliers_idx", u8, device),
-            None if c.outliers_val is None else _arg(c.outliers_val, "outliers_val", u8, device))
-
-
-def _call(func: str, device: int, stream, *args) -> None:
-    """The library's function on `stream` (None: the device's current one), with the device current."""
-    f = getattr(_lib_handle or lib(), func)
+def _call(func: str, like: torch.Tensor, stream, *args) -> None:
+    """The binding module's function on the device of `like`, which is made current, and on `stream` (None: the
+    device's current one)."""
+    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        raise ValueError("%s takes CUDA tensors" % func)
+    device = like.get_device()
+    f = getattr(_binding_module or _load_binding(), func)
     handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == device:
-        st = f(*args, handle)
+        st = f(device, handle, *args)
     else:
         with torch.cuda.device(device):
-            st = f(*args, handle)
+            st = f(device, handle, *args)
     if st != OK:
-        raise PqkvError(func, st)
+        raise PqkvError("pqkv_" + func, st)
 
 
 def paged_cross_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: int, cache: KVCache,
@@ -365,25 +362,9 @@ def paged_cross_attention(q: torch.Tensor, cu_q_lens: torch.Tensor, max_q_len: i
                           err_flag: torch.Tensor, kv_ranges: Optional[torch.Tensor] = None, stream=None) -> None:
     """pqkv_paged_cross_attention: q, out [T][Hq][D]; cu_q_lens int32 [B + 1]; block_tables int32
     [B][max_blocks] and kv_lens int32 [B] of the encoder's states; kv_ranges int32 [T][2] or None."""
-    dev, i32, dtype = _device_of(q, "q"), torch.int32, q.dtype
-    shape = q.shape
-    B, table = kv_lens.numel(), block_tables.shape
-    if len(shape) != 3 or out.shape != shape or shape[2] != cache.head_dim:
-        raise ValueError("q must be [T][num_q_heads][head_dim] of the cache's head_dim, and out match it")
-    if cu_q_lens.numel() != B + 1:
-        raise ValueError("cu_q_lens must be int32 [B + 1]")
-    if len(table) != 2 or table[0] != B:
-        raise ValueError("block_tables must be int32 [B][max_blocks_per_seq]")
-    if kv_ranges is not None and kv_ranges.shape != (shape[0], 2):
-        raise ValueError("kv_ranges must be int32 [T][2]")
-    if shape[0] == 0:
-        return
-    _call("pqkv_paged_cross_attention", dev, stream, _arg(q, "q", dtype, dev), _dt_of(q, "q"), B, max_q_len, shape[1],
-          _arg(cu_q_lens, "cu_q_lens", i32, dev), *_cache_args(cache, dev), cache.kv_dtype, cache.num_blocks,
-          cache.num_kv_heads, shape[2], _arg(block_tables, "block_tables", i32, dev), table[1],
-          _arg(kv_lens, "kv_lens", i32, dev),
-          None if kv_ranges is None else _arg(kv_ranges, "kv_ranges", i32, dev), scale,
-          _arg(out, "out", dtype, dev), _arg(err_flag, "err_flag", i32, dev))
+    _call("paged_cross_attention", q, stream, q, cu_q_lens, max_q_len, cache.cache, cache.scales, cache.outliers_idx,
+          cache.outliers_val, cache.kv_dtype, cache.num_blocks, cache.num_kv_heads, cache.head_dim, block_tables,
+          kv_lens, kv_ranges, scale, out, err_flag)
 
 
 def build_batch(start_pos: torch.Tensor, num_new: torch.Tensor, new_block_ids: torch.Tensor,
@@ -392,20 +373,8 @@ def build_batch(start_pos: torch.Tensor, num_new: torch.Tensor, new_block_ids: t
     """pqkv_build_batch: start_pos, num_new int32 [B] and new_block_ids int32 [n] on the device -> block_tables
     int32 [B][max_blocks] (in place), slot_mapping and positions int32 [max_tokens], cu_q_lens int32 [B + 1],
     seq_lens int32 [B]."""
-    dev, i32 = _device_of(start_pos, "start_pos"), torch.int32
-    B, capacity, table = start_pos.numel(), slot_mapping.numel(), block_tables.shape
-    if num_new.numel() != B or seq_lens.numel() != B or cu_q_lens.numel() != B + 1:
-        raise ValueError("num_new and seq_lens must be [B], cu_q_lens [B + 1]")
-    if len(table) != 2 or table[0] != B:
-        raise ValueError("block_tables must be int32 [B][max_blocks_per_seq]")
-    if positions.numel() != capacity:
-        raise ValueError("positions and slot_mapping must be of one size")
-    _call("pqkv_build_batch", dev, stream, _arg(start_pos, "start_pos", i32, dev), _arg(num_new, "num_new", i32, dev), B,
-          _arg(new_block_ids, "new_block_ids", i32, dev), new_block_ids.numel(),
-          _arg(block_tables, "block_tables", i32, dev), table[1], num_blocks, capacity,
-          _arg(slot_mapping, "slot_mapping", i32, dev), _arg(positions, "positions", i32, dev),
-          _arg(cu_q_lens, "cu_q_lens", i32, dev), _arg(seq_lens, "seq_lens", i32, dev),
-          _arg(err_flag, "err_flag", i32, dev))
+    _call("build_batch", start_pos, stream, start_pos, num_new, new_block_ids, block_tables, num_blocks, slot_mapping,
+          positions, cu_q_lens, seq_lens, err_flag)
 
 
 @dataclasses.dataclass
@@ -418,39 +387,7 @@ class Rotary:
     interleaved: bool = False
 
 
-def _heads(x: torch.Tensor, name: str, T: int, D: int, dtype: torch.dtype, device: int) -> Tuple[int, int, int]:
-    """Pointer, heads and token stride of [T][H][D] rows whose heads are contiguous within a token."""
-    shape, stride = x.shape, x.stride()
-    if len(shape) != 3 or shape[0] != T or shape[2] != D or stride[2] != 1 or (stride[1] != D and shape[1] > 1):
-        raise ValueError("%s must be [T][heads][head_dim] with contiguous heads" % name)
-    # the stride of a dimension of one token means nothing
-    return _arg(x, name, dtype, device, False), shape[1], stride[0] if T > 1 else shape[1] * D
-
-
-def _rotary_args(rotary: Optional[Rotary], positions: Optional[torch.Tensor], T: int, device: int):
-    """positions, num_axes, axis_of_pair, cos_sin, num_positions, rot_dim, interleaved."""
-    if rotary is None:
-        return None, 0, None, None, 0, 0, 0
-    table, axis = rotary.cos_sin, rotary.axis_of_pair
-    shape = table.shape
-    if len(shape) != 2:
-        raise ValueError("cos_sin must be float32 [num_positions][rot_dim]")
-    if shape[1] == 0:
-        return None, 0, None, None, 0, 0, 0
-    if axis and len(axis) != shape[1] // 2:
-        raise ValueError("axis_of_pair must hold rot_dim / 2 bytes")
-    if positions is None or len(positions.shape) not in (1, 2) or positions.shape[-1] != T:
-        raise ValueError("positions must be int32 [T] or [axes][T]")
-    return (_arg(positions, "positions", torch.int32, device), positions.numel() // max(1, T), axis or None,
-            _arg(table, "cos_sin", torch.float32, device), shape[0], shape[1], 1 if rotary.interleaved else 0)
-
-
-def _weight(w: Optional[torch.Tensor], name: str, D: int, device: int) -> Optional[int]:
-    if w is None:
-        return None
-    if w.numel() != D:
-        raise ValueError("%s must be float32 [head_dim]" % name)
-    return _arg(w, name, torch.float32, device)
+_NO_ROTATION = Rotary(None)
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -460,20 +397,9 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     """pqkv_qk_norm_rope: q [T][Hq][D] and k [T][Hkv][D] (or None), the heads of a token contiguous, any stride
     from one token to the next; positions int32 [T] or [axes][T]; q_out, k_out contiguous, or the input itself.
     A weight of None leaves the norm out, a rotary of None the rotation."""
-    dev, dtype = _device_of(q, "q"), q.dtype
-    if q.dim() != 3:
-        raise ValueError("q must be [T][num_q_heads][head_dim]")
-    T, _, D = q.shape
-    if T == 0:
-        return
-    if q_out.shape != q.shape or (k is None) != (k_out is None) or (k is not None and k_out.shape != k.shape):
-        raise ValueError("q_out and k_out must match q and k")
-    qp, Hq, qs = _heads(q, "q", T, D, dtype, dev)
-    kp, Hkv, ks = (None, 0, 0) if k is None else _heads(k, "k", T, D, dtype, dev)
-    _call("pqkv_qk_norm_rope", dev, stream, qp, kp, _dt_of(q, "q"), T, Hq, Hkv, D, qs, ks,
-          _weight(q_weight, "q_weight", D, dev), _weight(k_weight, "k_weight", D, dev), eps,
-          *_rotary_args(rotary, positions, T, dev), _arg(q_out, "q_out", dtype, dev),
-          None if k is None else _arg(k_out, "k_out", dtype, dev), _arg(err_flag, "err_flag", torch.int32, dev))
+    r = rotary or _NO_ROTATION
+    _call("qk_norm_rope", q, stream, q, k, q_weight, k_weight, eps, positions, r.cos_sin, r.axis_of_pair,
+          r.interleaved, q_out, k_out, err_flag)
 
 
 def qkv_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
@@ -482,26 +408,10 @@ def qkv_norm_rope_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, posit
                         k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, stream=None) -> None:
     """pqkv_qkv_norm_rope_write: qk_norm_rope whose keys, with the values v [T][Hkv][D], go to the cache slots
     of slot_mapping int32 [T] as kv_cache_write would store them."""
-    dev, dtype, i32 = _device_of(q, "q"), q.dtype, torch.int32
-    if q.dim() != 3:
-        raise ValueError("q must be [T][num_q_heads][head_dim]")
-    T, _, D = q.shape
-    if T == 0:
-        return
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must match q")
-    qp, Hq, qs = _heads(q, "q", T, D, dtype, dev)
-    kp, Hkv, ks = _heads(k, "k", T, D, dtype, dev)
-    vp, Hv, vs = _heads(v, "v", T, D, dtype, dev)
-    if Hkv != cache.num_kv_heads or Hv != Hkv or D != cache.head_dim:
-        raise ValueError("k and v must be [T][num_kv_heads][head_dim]")
-    if slot_mapping.numel() != T:
-        raise ValueError("slot_mapping must be int32 [T]")
-    _call("pqkv_qkv_norm_rope_write", dev, stream, qp, kp, vp, _dt_of(q, "q"), T, Hq, Hkv, D, qs, ks, vs,
-          _weight(q_weight, "q_weight", D, dev), _weight(k_weight, "k_weight", D, dev), eps,
-          *_rotary_args(rotary, positions, T, dev), _arg(q_out, "q_out", dtype, dev),
-          _arg(slot_mapping, "slot_mapping", i32, dev), *_cache_args(cache, dev), cache.kv_dtype, cache.num_blocks,
-          _arg(err_flag, "err_flag", i32, dev))
+    r = rotary or _NO_ROTATION
+    _call("qkv_norm_rope_write", q, stream, q, k, v, q_weight, k_weight, eps, positions, r.cos_sin, r.axis_of_pair,
+          r.interleaved, q_out, slot_mapping, cache.cache, cache.scales, cache.outliers_idx, cache.outliers_val,
+          cache.kv_dtype, cache.num_blocks, cache.num_kv_heads, cache.head_dim, err_flag)
 
 
 def encode(x: torch.Tensor, code_dtype: int, out: torch.Tensor, stream=None) -> None:

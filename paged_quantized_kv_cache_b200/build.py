@@ -4,7 +4,9 @@
 
 Every .cu / .cpp under csrc/ is compiled to an object in _build/ (in parallel)
 and linked into paged_quantized_kv_cache_b200/libpqkv.so with the static CUDA
-runtime. No GPU is needed to build.
+runtime; csrc/python/binding.cpp (the Python binding's argument marshalling)
+becomes paged_quantized_kv_cache_b200/_binding.so with the host compiler. No GPU
+is needed to build.
 """
 from __future__ import annotations
 
@@ -15,12 +17,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libpqkv.so")
+BINDING_SRC = os.path.join(CSRC, "python", "binding.cpp")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -46,6 +51,19 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_command(out: str):
+    """Host compile of the Python module against the headers and libraries of the running Python and torch (which
+    its process has loaded before it)."""
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    libs = ["-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    include = [sysconfig.get_paths()["include"], base, os.path.join(base, "torch", "csrc", "api", "include"),
+               os.path.join(ROOT, "include")]
+    abi = "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi())
+    return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", abi,
+            *("-isystem" + i for i in include), BINDING_SRC, "-o", out, *libs]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -62,6 +80,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(obj, [src] + headers):
             jobs.append([nvcc] + flags + ["-c", src, "-o", obj])
 
+    binding_tmp = BINDING + ".tmp%d" % os.getpid()
+    make_binding = force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pqkv.h"), __file__])
+    if make_binding:
+        jobs.append(_binding_command(binding_tmp))
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -75,7 +98,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 failed.append(cmd[-3])
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
-    if force or jobs or _stale(LIB, objs):
+    if make_binding:
+        os.replace(binding_tmp, BINDING)
+    if force or _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -188,8 +188,8 @@ bool out_ok(const Heads& out, const Heads* in, int n_in, int own, int T, int D) 
   return true;
 }
 
-// CTAs of the rotary kernel fit a grid (8 warps of at least 8 rows of a token each).
-bool rope_grid_ok(int64_t T, int64_t rows) { return T * ((rows + 7) / 8) / 8 < INT32_MAX - 8; }
+// The rotary kernel's grid: a row of CTAs for each chunk of at least 8 heads.
+bool rope_grid_ok(int64_t heads) { return heads / 8 + 3 <= 65535; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -634,7 +634,7 @@ int pqkv_qk_norm_rope(const void* q, const void* k, int dtype, int num_tokens, i
   const int T = num_tokens, D = head_dim;
   if (rope_params(p.r, dtype, T, num_q_heads, D, q_weight, k_weight, eps, positions, num_axes, axis_of_pair, cos_sin,
                   num_positions, rot_dim, interleaved) != PQKV_OK ||
-      num_kv_heads < 0 || !rope_grid_ok(T, (int64_t)num_q_heads + num_kv_heads))
+      num_kv_heads < 0 || !rope_grid_ok((int64_t)num_q_heads + num_kv_heads))
     return PQKV_ERR_ARG;
   if (T == 0) return PQKV_OK;
   const Heads in[2] = {{q, num_q_heads, q_stride}, {num_kv_heads ? k : nullptr, num_kv_heads, k_stride}};
@@ -652,7 +652,7 @@ int pqkv_qk_norm_rope(const void* q, const void* k, int dtype, int num_tokens, i
   p.err = err_flag;
   p.Hq = num_q_heads;
   p.Hkv = num_kv_heads;
-  p.rows = num_q_heads + num_kv_heads;
+  p.kinds = num_kv_heads > 0 ? 1 : 0;
   const cudaError_t e =
       launch_rope(dtype == PQKV_DTYPE_BF16, D, interleaved != 0, p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
@@ -671,7 +671,7 @@ int pqkv_qkv_norm_rope_write(const void* q, const void* k, const void* v, int dt
   const int T = num_tokens, D = head_dim;
   if (rope_params(p.r, dtype, T, num_q_heads, D, q_weight, k_weight, eps, positions, num_axes, axis_of_pair, cos_sin,
                   num_positions, rot_dim, interleaved) != PQKV_OK ||
-      num_kv_heads < 1 || num_kv_heads > 65535 || !rope_grid_ok(T, (int64_t)num_q_heads + 2 * (int64_t)num_kv_heads))
+      num_kv_heads < 1 || num_kv_heads > 65535 || !rope_grid_ok((int64_t)num_q_heads + 2 * (int64_t)num_kv_heads))
     return PQKV_ERR_ARG;
   if (!is_kv_dtype(kv_dtype) || (is_16(kv_dtype) && dtype != kv_dtype) || num_blocks < 1 ||
       (int64_t)num_blocks * PQKV_BLOCK_SIZE > INT32_MAX)
@@ -700,7 +700,7 @@ int pqkv_qkv_norm_rope_write(const void* q, const void* k, const void* v, int dt
   p.Hq = num_q_heads;
   p.Hkv = num_kv_heads;
   p.nb = num_blocks;
-  p.rows = is_16(kv_dtype) ? num_q_heads + 2 * num_kv_heads : num_q_heads;
+  p.kinds = is_16(kv_dtype) ? 2 : 0;
   cudaError_t e = launch_rope(dtype == PQKV_DTYPE_BF16, D, interleaved != 0, p, st);
   if (e == cudaSuccess && !is_16(kv_dtype)) {
     WriteParams w;

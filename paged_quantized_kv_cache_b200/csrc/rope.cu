@@ -12,96 +12,102 @@
 // lanes hold a row, four pairs each (two 8-byte pieces, or one of 16 bytes for
 // neighbouring pairs), so a rotation needs no exchange between lanes and the
 // norm one tree of log2(D / 8) shuffles. A warp takes kUnroll rows per lane of
-// one token at once: their loads are all in flight before the first sum, and
-// the token's positions, cosines and sines are read once for them.
+// one token, all of one kind (queries, keys or values: blockIdx.y): their loads
+// are all in flight before the first sum, and the token's positions, cosines
+// and sines and the kind's weights are read once for them.
 #include "rope.cuh"
 
 namespace pqkv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kUnroll = 4;
 
+// Chunks of kUnroll rows per lane that `heads` rows of a token take.
+template <int D>
+__host__ __device__ constexpr int chunks_of(int heads) {
+  return (heads + 256 / D * kUnroll - 1) / (256 / D * kUnroll);
+}
+
 template <int D, bool BF16, bool IL>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 10) rope_kernel(const __grid_constant__ RopeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int kLanes = D / 8;          // lanes of a row
-  constexpr int kRows = 32 / kLanes;     // rows a warp holds at once
-  constexpr int kChunk = kRows * kUnroll;
+  constexpr int kLanes = D / 8;       // lanes of a row
+  constexpr int kRows = 32 / kLanes;  // rows a warp holds at once
   const int lane = threadIdx.x & 31;
-  const int chunks = (p.rows + kChunk - 1) / kChunk;
-  const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  const int t = (int)(unit / chunks);
+  const int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   if (t >= p.r.T) return;
-  const int row0 = (int)(unit % chunks) * kChunk + lane / kLanes;
+  int chunk = blockIdx.y, heads = p.Hq;
+  const bool is_q = chunk < chunks_of<D>(p.Hq);
+  bool is_v = false;
+  if (!is_q) {
+    chunk -= chunks_of<D>(p.Hq);
+    heads = p.Hkv;
+    is_v = chunk >= chunks_of<D>(p.Hkv);
+    if (is_v) chunk -= chunks_of<D>(p.Hkv);
+  }
+  const int row0 = chunk * kRows * kUnroll + lane / kLanes;
   const int i0 = 4 * (lane % kLanes);
   int a, b;
   pair_channels<D, IL>(i0, p.r.rot, a, b);
 
+  int pos[kMaxAxes];
+  if (!is_v) load_positions(p.r, t, pos);
+  int slot = -1;
+  if (!is_q && !p.k_out) slot = __ldg(p.slots + t);
+  const uint16_t* src = is_q ? static_cast<const uint16_t*>(p.q) + (size_t)t * p.qs
+                      : is_v ? static_cast<const uint16_t*>(p.v) + (size_t)t * p.vs
+                             : static_cast<const uint16_t*>(p.k) + (size_t)t * p.ks;
   uint4 raw[kUnroll];
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int row = row0 + u * kRows;
-    raw[u] = make_uint4(0, 0, 0, 0);
-    if (row < p.rows) {
-      const uint16_t* src;
-      if (row < p.Hq)
-        src = static_cast<const uint16_t*>(p.q) + (size_t)t * p.qs + (size_t)row * D;
-      else if (row < p.Hq + p.Hkv)
-        src = static_cast<const uint16_t*>(p.k) + (size_t)t * p.ks + (size_t)(row - p.Hq) * D;
-      else
-        src = static_cast<const uint16_t*>(p.v) + (size_t)t * p.vs + (size_t)(row - p.Hq - p.Hkv) * D;
-      raw[u] = load_pairs<IL>(src, a, b);
+    raw[u] = row < heads ? load_pairs<IL>(src + (size_t)row * D, a, b) : make_uint4(0, 0, 0, 0);
+  }
+  // where the rows go: heads of a token follow one another in an output, and lie
+  // two tiles of a block apart in the cache
+  uint16_t* dst;
+  size_t step = D;
+  if (is_q) {
+    dst = static_cast<uint16_t*>(p.q_out) + (size_t)t * p.Hq * D;
+  } else if (p.k_out) {
+    dst = static_cast<uint16_t*>(p.k_out) + (size_t)t * p.Hkv * D;
+  } else {
+    if (slot >= p.nb * kBlock && !is_v && chunk == 0 && lane == 0) raise_flag(p.err, PQKV_DEVERR_SLOT);
+    if (slot < 0 || slot >= p.nb * kBlock) return;
+    step = 2 * kBlock * D;
+    dst = reinterpret_cast<uint16_t*>(p.cache) +
+          (((size_t)(slot >> 4) * p.Hkv * 2 + (is_v ? 1 : 0)) * kBlock + (slot & 15)) * D;
+  }
+  if (is_v) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int row = row0 + u * kRows;
+      if (row < heads) store_pairs<IL>(dst + row * step, a, b, raw[u]);
     }
+    return;
   }
   Pairs cs;
-  const bool ok = load_angles<D>(p.r, t, i0, cs);
-  if (!ok && lane == 0 && row0 == 0) raise_flag(p.err, PQKV_DEVERR_POSITION);
-  int slot = -1;
-  if (!p.k_out && p.rows > p.Hq) {
-    slot = __ldg(p.slots + t);
-    if (slot >= p.nb * kBlock) {
-      if (lane == 0 && row0 == 0) raise_flag(p.err, PQKV_DEVERR_SLOT);
-      slot = -1;
-    }
-  }
+  const bool ok = load_angles(p.r, pos, i0, cs);
+  if (!ok && lane == 0 && chunk == 0) raise_flag(p.err, PQKV_DEVERR_POSITION);
+  const float* weight = is_q ? p.r.q_weight : p.r.k_weight;
+  Pairs w = {};
+  if (weight) w = load_weight<IL>(weight, a, b);
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int row = row0 + u * kRows;
-    const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.Hkv;
-    const float* weight = is_q ? p.r.q_weight : p.r.k_weight;
-    const bool norm = weight != nullptr && !is_v;
-    Pairs w = {};
-    if (norm && row < p.rows) w = load_weight<IL>(weight, a, b);
-    const Pairs x = unpack_pairs<BF16, IL>(raw[u]);
-    const Pairs z = norm_rotate<D>(x, norm, w, p.r.eps, 2 * i0 < p.r.rot, cs);
-    if (row >= p.rows) continue;
-    uint4 out = is_v ? raw[u] : pack_pairs<BF16, IL>(z);
-    if (!ok && !is_v) out = make_uint4(0, 0, 0, 0);
-    uint16_t* dst;
-    if (is_q) {
-      dst = static_cast<uint16_t*>(p.q_out) + ((size_t)t * p.Hq + row) * D;
-    } else if (p.k_out) {
-      dst = static_cast<uint16_t*>(p.k_out) + ((size_t)t * p.Hkv + (row - p.Hq)) * D;
-    } else {
-      if (slot < 0) continue;
-      const int h = is_v ? row - p.Hq - p.Hkv : row - p.Hq;
-      dst = reinterpret_cast<uint16_t*>(p.cache) +
-            ((((size_t)(slot >> 4) * p.Hkv + h) * 2 + (is_v ? 1 : 0)) * kBlock + (slot & 15)) * D;
-    }
-    store_pairs<IL>(dst, a, b, out);
+    const Pairs z = norm_rotate<D>(unpack_pairs<BF16, IL>(raw[u]), weight != nullptr, w, p.r.eps, 2 * i0 < p.r.rot, cs);
+    if (row < heads) store_pairs<IL>(dst + row * step, a, b, ok ? pack_pairs<BF16, IL>(z) : make_uint4(0, 0, 0, 0));
   }
 }
 
 template <int D, bool BF16, bool IL>
 cudaError_t launch_rope_t(const RopeParams& p, cudaStream_t st) {
-  constexpr int kChunk = 32 / (D / 8) * kUnroll;
-  const long long units = (long long)p.r.T * ((p.rows + kChunk - 1) / kChunk);
-  const long long grid = (units + kThreads / 32 - 1) / (kThreads / 32);
+  const int chunks = chunks_of<D>(p.Hq) + p.kinds * chunks_of<D>(p.Hkv);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)((p.r.T + kThreads / 32 - 1) / (kThreads / 32)), (unsigned)chunks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -116,7 +122,7 @@ cudaError_t launch_rope_t(const RopeParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_rope(bool bf16, int D, bool interleaved, const RopeParams& p, cudaStream_t st) {
-  if (p.r.T == 0 || p.rows == 0) return cudaSuccess;
+  if (p.r.T == 0) return cudaSuccess;
 #define PQKV_ROPE(DD, BF, IL) \
   if (D == DD && bf16 == BF && interleaved == IL) return launch_rope_t<DD, BF, IL>(p, st);
   PQKV_ROPE(128, true, false)

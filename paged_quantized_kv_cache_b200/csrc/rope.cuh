@@ -31,7 +31,7 @@ struct RopeParams {
   uint8_t* cache;        // 16-bit cache
   int32_t* err;
   int Hq, Hkv, nb;
-  int rows;              // rows per token that the kernel takes: Hq, Hq + Hkv or Hq + 2 Hkv
+  int kinds;             // 0: queries only, 1: and keys, 2: and values
 };
 
 cudaError_t launch_rope(bool bf16, int D, bool interleaved, const RopeParams& p, cudaStream_t st);
@@ -105,10 +105,15 @@ __device__ __forceinline__ Pairs load_weight(const float* w, int a, int b) {
   return Pairs{{x.x, x.y, x.z, x.w}, {y.x, y.y, y.z, y.w}};
 }
 
-// Cosines (a) and sines (b) of pairs i0 .. i0 + 3 of token t. False if one of
-// the token's positions lies outside the table.
-template <int D>
-__device__ __forceinline__ bool load_angles(const RowParams& r, int t, int i0, Pairs& cs) {
+// Token t's positions on the axes.
+__device__ __forceinline__ void load_positions(const RowParams& r, int t, int (&pos)[kMaxAxes]) {
+#pragma unroll
+  for (int x = 0; x < kMaxAxes; ++x) pos[x] = (r.rot > 0 && x < r.axes) ? __ldg(r.positions + (size_t)x * r.T + t) : 0;
+}
+
+// Cosines (a) and sines (b) of pairs i0 .. i0 + 3 at these positions. False if
+// one of them lies outside the table.
+__device__ __forceinline__ bool load_angles(const RowParams& r, const int (&pos)[kMaxAxes], int i0, Pairs& cs) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     cs.a[e] = 1.f;
@@ -116,12 +121,8 @@ __device__ __forceinline__ bool load_angles(const RowParams& r, int t, int i0, P
   }
   if (r.rot == 0) return true;
   bool ok = true;
-  int pos[kMaxAxes];
 #pragma unroll
-  for (int x = 0; x < kMaxAxes; ++x) {
-    pos[x] = x < r.axes ? __ldg(r.positions + (size_t)x * r.T + t) : 0;
-    ok = ok && pos[x] >= 0 && pos[x] < r.num_pos;
-  }
+  for (int x = 0; x < kMaxAxes; ++x) ok = ok && pos[x] >= 0 && pos[x] < r.num_pos;
   const int half = r.rot / 2;
   if (!ok || i0 >= half) return ok;
   const uint32_t ax = r.axis[i0 >> 2];

@@ -100,7 +100,9 @@ __device__ __forceinline__ void stage_run(const WriteParams& p, int ts, int n, i
     }
     if (kv == 0) {
       Pairs cs = {};
-      const bool ok = !mine || load_angles<D>(p.rope, ts + j, i0, cs);
+      int pos[kMaxAxes];
+      if (mine) load_positions(p.rope, ts + j, pos);
+      const bool ok = !mine || load_angles(p.rope, pos, i0, cs);
       const Pairs z = norm_rotate<D>(unpack_pairs<BF16, IL>(raw), norm, w, p.rope.eps, 2 * i0 < p.rope.rot, cs);
       raw = ok ? pack_pairs<BF16, IL>(z) : make_uint4(0, 0, 0, 0);
     }

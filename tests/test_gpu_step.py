@@ -87,3 +87,51 @@ def test_chunk_then_decode_steps(kv_dtype, dtype):
         assert (np.abs(cross_out[:T].double().cpu().numpy() - want) <= tol).all()
         assert (cross_out[T:] == 0).all()
         start += new
+
+
+def test_calls_refuse_tensors_that_they_do_not_take():
+    """Types, shapes, strides and devices that the Python calls refuse, with the outputs left alone."""
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")  # noqa: E731
+    x = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    err, out = i32(1), torch.full_like(x, 7)
+    table = pq.Rotary(torch.zeros(8, 64, device="cuda"))
+    p = i32(4)
+    c = pq.allocate_cache(pq.BF16, 2, 2, 64)
+    bad = [
+        lambda: pq.build_batch(i32(2), i32(3), i32(1), i32(2, 4), 9, i32(5), i32(5), i32(3), i32(2), err),
+        lambda: pq.build_batch(i32(2), i32(2), i32(1), i32(2, 4), 9, i32(5), i32(4), i32(3), i32(2), err),
+        lambda: pq.build_batch(i32(2), i32(2), i32(1), i32(8), 9, i32(5), i32(5), i32(3), i32(2), err),
+        lambda: pq.build_batch(i32(2), i32(2).long(), i32(1), i32(2, 4), 9, i32(5), i32(5), i32(3), i32(2), err),
+        lambda: pq.build_batch(i32(2), i32(2), i32(1), i32(2, 8)[:, ::2], 9, i32(5), i32(5), i32(3), i32(2), err),
+        lambda: pq.build_batch(i32(2), i32(2), i32(1).cpu(), i32(2, 4), 9, i32(5), i32(5), i32(3), i32(2), err),
+        lambda: pq.build_batch(i32(2), i32(2), i32(1), i32(2, 4), 2 ** 40, i32(5), i32(5), i32(3), i32(2), err),
+        lambda: pq.qk_norm_rope(x, x.half(), p, table, out, out, err),
+        lambda: pq.qk_norm_rope(x, None, p, table, out, out, err),
+        lambda: pq.qk_norm_rope(x, None, p[:3], table, out, None, err),
+        lambda: pq.qk_norm_rope(x, None, None, table, out, None, err),
+        lambda: pq.qk_norm_rope(x, None, p, pq.Rotary(table.cos_sin, b"\0"), out, None, err),
+        lambda: pq.qk_norm_rope(x, None, p, pq.Rotary(table.cos_sin.double()), out, None, err),
+        lambda: pq.qk_norm_rope(x.transpose(0, 1), None, p, table, out.transpose(0, 1), None, err),
+        lambda: pq.qk_norm_rope(x, None, p, table, out, None, err, q_weight=torch.ones(63, device="cuda")),
+        lambda: pq.qk_norm_rope(x, None, p, table, out, None, err, q_weight=torch.ones(64)),
+        lambda: pq.qk_norm_rope(x, None, p, table, out.float(), None, err),
+        lambda: pq.qkv_norm_rope_write(x, x, x[:, :1], p, table, out, p, c, err),
+        lambda: pq.qkv_norm_rope_write(x, x, x, p, table, out, p[:2], c, err),
+        lambda: pq.paged_cross_attention(x, i32(3), 1, c, i32(1, 1), i32(1), 1.0, out, err),
+        lambda: pq.paged_cross_attention(x, i32(2), 1, c, i32(1, 1), i32(1), 1.0, out, err, kv_ranges=i32(3, 2)),
+        lambda: pq.paged_cross_attention(x, i32(2), "1", c, i32(1, 1), i32(1), 1.0, out, err),
+        lambda: pq.paged_cross_attention(x, i32(2), 1, c, i32(1, 1), i32(1), 1.0, out, None),
+    ]
+    for k, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError("call %d was taken" % k)
+    with pytest.raises(pq.PqkvError):
+        pq.paged_cross_attention(x, i32(2), 0, c, i32(1, 1), i32(1), 1.0, out, err)
+    torch.cuda.synchronize()
+    assert (out == 7).all() and int(err.item()) == 0
+    for empty in (pq.qk_norm_rope, None):  # no tokens: nothing to do
+        if empty:
+            pq.qk_norm_rope(x[:0], x[:0], p[:0], table, out[:0], out[:0], err)
+        else:
+            pq.paged_cross_attention(x[:0], i32(2), 1, c, i32(1, 1), i32(1), 1.0, out[:0], err)

@@ -56,7 +56,7 @@ BAD_ROPE = [
 
 
 @pytest.mark.parametrize("bad", BAD_ROPE + [
-    dict(hkv=-1), dict(k_out=None), dict(k_out=A), dict(k_out=4 * A), dict(T=2 ** 31 - 1, hq=1024, qs=65536)], ids=str)
+    dict(hkv=-1), dict(k_out=None), dict(k_out=A), dict(k_out=4 * A), dict(hq=1 << 20, qs=1 << 26)], ids=str)
 def test_norm_rope_refuses(bad):
     assert _rope(**bad) == pq.ERR_ARG
 
@@ -108,6 +108,18 @@ def test_bindings_refuse_host_tensors():
         pq.qkv_norm_rope_write(x, x, x, None, None, x, i, c, i)
     with pytest.raises(ValueError):
         pq.paged_cross_attention(x, i, 1, c, i.view(2, 2), i, 1.0, x, i)
+
+
+def test_binding_module_loads_and_refuses():
+    """Its checks without a GPU: argument counts, types, tensors of the host (a device index of -1 matches none)."""
+    m = pq._load_binding()
+    x, i = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    for call, args in ((m.build_batch, (0, 0, i)), (m.build_batch, (0, 0) + (i,) * 10), (m.build_batch, (-1, 0) + (i,) * 10),
+                       (m.qk_norm_rope, (0, 0, x, x, None, None, 1e-6, None, None, b"", False, x, x, i)),
+                       (m.qk_norm_rope, (0, 0, 3, x, None, None, 1e-6, None, None, b"", False, x, x, i)),
+                       (m.paged_cross_attention, ("a", 0) + (x,) * 17), (m.qkv_norm_rope_write, ())):
+        with pytest.raises(ValueError):
+            call(*args)
 
 
 def test_plain_batch_agrees_with_the_host_slot_mapping():
