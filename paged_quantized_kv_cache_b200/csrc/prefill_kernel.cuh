@@ -206,6 +206,10 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
   using Gm = PrefillGeom<KVF, D>;
   constexpr int NWG = Gm::NWG, kStages = Gm::kStages;
   constexpr bool kBfMma = (KVF == PQKV_DTYPE_BF16);  // operand type: bf16 for a bf16 cache, else f16
+  // CROSS keeps P in one part whatever its type: half a step of bf16 (2^-8 of p)
+  // in the weights of a mean is what the 16-bit output itself is rounded by, and
+  // P_lo costs half as much tensor-core work again (cross.cu)
+  constexpr bool kSplitP = Gm::kSplitP && !CROSS;
   constexpr uint32_t kIdescS = tc::f16_idesc(kBfMma, kM, kN, false);
   constexpr uint32_t kIdescPV = tc::f16_idesc(kBfMma, kM, D, true);
 
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
         for (int kk = 0; kk < kN / 16; ++kk) {
           const uint64_t bd = tc::sw128_desc(va + kk * 2048, kN * 128, 1024);
           tc::mma_ts(o, pa + kk * 8, bd, kIdescPV, !(t == 0 && kk == 0));
-          if constexpr (Gm::kSplitP) tc::mma_ts(o, pa + 32 + kk * 8, bd, kIdescPV, true);
+          if constexpr (kSplitP) tc::mma_ts(o, pa + 32 + kk * 8, bd, kIdescPV, true);
         }
         tc::commit(&bar_pv[2 * w + (t & 1)]);
         if constexpr (!Gm::k16) tc::commit(&bar_vfree[t % 3]);  // the V operand buffer may be refilled
@@ -682,13 +686,15 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
     auto leave = [&]() -> bool { return !__all_sync(kFull, ok); };
     float m = -INFINITY, l = 0.f, vref = 0.f;
     float rvref = 0.f;  // FP8: 1 / vref (0 while vref is 0), recomputed only when vref grows
-    if constexpr (Gm::k16) {
-      if (!CROSS || T > 0) mask_next = prepare(0);
+    if constexpr (Gm::k16 && !CROSS) {
+      mask_next = prepare(0);
       if (leave()) aborted = true;
     }
 
     for (int t = 0; t < T && !aborted; ++t) {
-      if constexpr (Gm::k16) {
+      if constexpr (Gm::k16 && CROSS) {
+        mask_cur = prepare(t);
+      } else if constexpr (Gm::k16) {
         mask_cur = mask_next;
         if (t + 1 < T) mask_next = prepare(t + 1);
       }
@@ -704,6 +710,64 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
 
       // scores of this row
       const uint32_t t_s = t_row + D + 64 * (t & 1);
+      if constexpr (CROSS) {
+        // The usual tile: every row of the warp sees all of it or nothing, and
+        // has a max from earlier tiles. That max then stays: exponents are taken
+        // against it while the scores arrive, 16 columns (a cache block) at a
+        // time, and only a row sum that shows a much larger score sends the warp
+        // through the general way below, from the same scores. A row that sees
+        // nothing gets an argument of 0 x - inf.
+        const int base = (t0 + t) * kN;
+        const bool none = !row_ok || my_hi <= base || my_lo >= base + kN;
+        const bool whole = my_lo <= base && base + kN <= my_hi;
+        bool usual = mask_cur == 0xF && base + kN <= L && __all_sync(kFull, none || (whole && m != -INFINITY));
+        float cj[4], vr[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          cj[j] = sl2;
+          vr[j] = 1.f;
+          if constexpr (Gm::kFp8) {
+            const float k = tile_sk[(t & 3) * 4 + j], v = tile_sv[(t & 3) * 4 + j];
+            cj[j] *= k;
+            vr[j] = v * rvref;
+            usual = usual && v <= vref;  // the same on every thread
+          }
+          if (none) cj[j] = 0.f;
+        }
+        if (usual) {
+          const float nm = none ? -INFINITY : -m;
+          uint32_t pk[32];
+          float ra[2] = {0.f, 0.f}, rb[2] = {0.f, 0.f};
+          uint32_t x[2][16];
+          tc::tmem_ld16_start(t_s, x[0]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            tc::tmem_ld_wait(x[j & 1]);
+            if (j < 3) tc::tmem_ld16_start(t_s + 16 * (j + 1), x[(j + 1) & 1]);
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              float ya, yb;
+              fma2(ya, yb, __uint_as_float(x[j & 1][c]), __uint_as_float(x[j & 1][c + 1]), cj[j], cj[j], nm, nm);
+              float pa = ex2(ya), pb = ex2(yb);
+              const int i = (c >> 1) & 1;
+              add2(ra[i], rb[i], ra[i], rb[i], pa, pb);
+              if constexpr (Gm::kFp8) mul2(pa, pb, pa, pb, vr[j], vr[j]);
+              pk[8 * j + (c >> 1)] = pack_f32x2(pa, pb, kBfMma);
+            }
+          }
+          const float sum = (ra[0] + ra[1]) + (rb[0] + rb[1]);
+          // f16 holds P up to 65504; bf16 has the range of fp32
+          constexpr float kMost = kBfMma ? 0x1p60f : 0x1p15f;
+          if (__all_sync(kFull, sum <= kMost)) {
+            l += sum;
+            tc::tmem_st32(t_s, pk);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&my_p[t & 1]);
+            continue;
+          }
+        }
+      }
       uint32_t sv[64];
       tc::tmem_ld64(t_s, sv);
       const int mask = mask_cur;
@@ -798,7 +862,7 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
           float wa = pa, wb = pb;
           if constexpr (Gm::kFp8) mul2(wa, wb, pa, pb, vr[c >> 4], vr[c >> 4]);
           pk[c >> 1] = pack_f32x2(wa, wb, kBfMma);
-          if constexpr (Gm::kSplitP) {
+          if constexpr (kSplitP) {
             float da, db;
             sub2(da, db, wa, wb, unpack_lo(pk[c >> 1], kBfMma), unpack_hi(pk[c >> 1], kBfMma));
             pl[c >> 1] = pack_f32x2(da, db, kBfMma);
@@ -824,7 +888,7 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
       }
       // P row -> tensor memory over this row's S(t) (P_hi, then P_lo for bf16),
       // then this warp's share of P(t) is handed to its warpgroup's MMA warp
-      if constexpr (Gm::kSplitP) {
+      if constexpr (kSplitP) {
         uint32_t pp[64];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {

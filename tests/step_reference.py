@@ -83,13 +83,14 @@ def rope_tolerance(z, size, dtype):
     return HALF[dtype] * np.abs(z) + (1 + HALF[dtype]) * 2.0 ** -20 * size + TINY[dtype]
 
 
-def cross(cache, q, cu, tables, lens, scale, ranges=None):
+def cross(cache, q, cu, tables, lens, scale, ranges=None, max_q_len=None):
     """(out, tolerance) in 64 bits over the oracle's dequantized states. The tolerance adds up the kernel's
     roundings, with A = sum p |v| of a row and one output channel:
       output             HALF |out|
       P                  half a step of its type relative to p: f16 2^-11 A (plus, for p below 2^-14, 2^-25 |v| a
                          key, over a row sum of at least 1, and twice that where FP8's V scales differ by up
-                         to 2); bf16 caches keep P_hi + P_lo: (2^-8)^2 A
+                         to 2); bf16 2^-8 A, and where a KV head has at most 16
+                         query rows P_hi + P_lo, (2^-8)^2 A
       scores             fp32 sums of D exact products, D 2^-24 sum |q k| scale, and the exponent's argument and
                          2^x, 4 * 2^-24 (|score| log2 e + 8): each shifts p and the row sum, so twice
       sums over L keys   L 2^-24 A, in O and in the row sum, so twice
@@ -99,6 +100,8 @@ def cross(cache, q, cu, tables, lens, scale, ranges=None):
     out, tol = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
     H = cache.H
     f16_p = cache.dt != oracle.DT_BF16
+    most = max_q_len or max(int(x) for x in np.diff(cu))
+    half_p = 2.0 ** -11 if f16_p else 2.0 ** -16 if most * (Hq // H) <= 16 else 2.0 ** -8
     for b, L in enumerate(int(x) for x in lens):
         rows = slice(int(cu[b]), int(cu[b + 1]))
         if rows.start == rows.stop or L <= 0 or L > BLOCK * tables.shape[1]:
@@ -121,7 +124,7 @@ def cross(cache, q, cu, tables, lens, scale, ranges=None):
                 o, mag = p @ v, p @ np.abs(v)
                 shift = np.where(seen, D * 2.0 ** -24 * size + 4 * 2.0 ** -24 * (np.abs(np.where(seen, s, 0)) * 1.4427 + 8),
                                  0).max(-1, keepdims=True)
-                rel = (2.0 ** -11 if f16_p else 2.0 ** -16) + 2 * shift + 2 * L * 2.0 ** -24 + 2.0 ** -22
+                rel = half_p + 2 * shift + 2 * L * 2.0 ** -24 + 2.0 ** -22
                 out[rows, n] = o
                 tol[rows, n] = HALF[q.dtype] * np.abs(o) + (1 + HALF[q.dtype]) * (
                     rel * mag + (2.0 ** -24 * np.abs(v).sum(0) if f16_p else 0)) + TINY[q.dtype]
