@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
   uint64_t* bar_kfree = bar_op + 4;          // [2] quantized: S(t) of every warpgroup done (kop[t % 2])
   uint64_t* bar_vfree = bar_kfree + 2;       // [3] quantized: PV(t) of every warpgroup done (vop[t % 3])
   uint64_t* bar_drain = bar_vfree + 3;       // [NWG] every product an MMA warp issued has completed
-  float* tile_sk = reinterpret_cast<float*>(bar_drain + NWG);  // [4][4] FP8 K scales of tile t % 4
+  static_assert((2 * kStages + 6 * NWG + 4 + 2 + 3 + NWG) % 2 == 1, "the scales behind the barriers and a word");
+  float* tile_sk = reinterpret_cast<float*>(bar_drain + NWG + 1);  // [4][4] FP8 K scales of tile t % 4 (16-byte rows)
   float* tile_sv = tile_sk + 16;                               // [4][4] FP8 V scales
   volatile int* op_mask = reinterpret_cast<volatile int*>(tile_sv + 16);  // [4] quantized: blocks of tile t % 4
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(op_mask) + 4);
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
     auto prepare = [&](int t) -> int {
       const int s = t % kStages;
       ok = mbar_wait_bounded(&bar_full[s], (uint32_t)(t / kStages) & 1u, p.timeout_ns) && ok;
-      if (ok) ++n_prepared;  // counted up to the first wait that gave up: the drain covers the rest
+      if (!CROSS && ok) ++n_prepared;  // counted up to the first wait that gave up: the drain covers the rest
       // blocks of the tile that were fetched, as the producer left them beside
       // the stage (after a timeout the value may be stale: it is the same for
       // every thread, and the results are not used then)
@@ -686,26 +687,54 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
     auto leave = [&]() -> bool { return !__all_sync(kFull, ok); };
     float m = -INFINITY, l = 0.f, vref = 0.f;
     float rvref = 0.f;  // FP8: 1 / vref (0 while vref is 0), recomputed only when vref grows
+    // CROSS: tiles [whole_lo, whole_hi) lie inside this row's range, tiles below
+    // none_hi and from none_lo on outside it; tiles below t_full end inside the states
+    int whole_lo = 0, whole_hi = 0, none_hi = T, none_lo = 0;
+    const int t_full = L / kN - t0;
+    if (CROSS && row_ok && my_lo < my_hi) {
+      whole_lo = (my_lo + kN - 1) / kN - t0;
+      whole_hi = my_hi / kN - t0;
+      none_hi = my_lo / kN - t0;
+      none_lo = (my_hi + kN - 1) / kN - t0;
+    }
     if constexpr (Gm::k16 && !CROSS) {
       mask_next = prepare(0);
       if (leave()) aborted = true;
     }
 
     for (int t = 0; t < T && !aborted; ++t) {
-      if constexpr (Gm::k16 && CROSS) {
-        mask_cur = prepare(t);
-      } else if constexpr (Gm::k16) {
-        mask_cur = mask_next;
-        if (t + 1 < T) mask_next = prepare(t + 1);
+      bool usual = false;  // CROSS: see below
+      if constexpr (CROSS) {
+        // S(t) done: its MMA warp saw the tile's operands, mask and scales, so
+        // they are visible here too
+        ok = (mbar_test_wait(&my_s[t & 1], (uint32_t)(t >> 1) & 1u) ||
+              mbar_wait_bounded(&my_s[t & 1], (uint32_t)(t >> 1) & 1u, p.timeout_ns)) && ok;
+        mask_cur = Gm::k16 ? stage_mask[t % kStages] : op_mask[t & 3];
+        const bool whole = t >= whole_lo && t < whole_hi, none = t < none_hi || t >= none_lo;
+        usual = __all_sync(kFull, ok && mask_cur == 0xF && t < t_full && (none || (whole && m != -INFINITY)));
+        if (!usual) {
+          if (leave()) {
+            aborted = true;
+            break;
+          }
+          if constexpr (Gm::k16)
+            if (mask_cur != 0xF || t >= t_full) (void)prepare(t);
+        }
+        if constexpr (Gm::k16) ++n_prepared;  // its copies have landed
+      } else {
+        if constexpr (Gm::k16) {
+          mask_cur = mask_next;
+          if (t + 1 < T) mask_next = prepare(t + 1);
+        }
+        ok = mbar_wait_bounded(&my_s[t & 1], (uint32_t)(t >> 1) & 1u, p.timeout_ns) && ok;
+        // quantized: the tile's block mask and FP8 scales, left by the dequantization
+        if constexpr (!Gm::k16) ok = mbar_wait_bounded(&bar_op[t & 3], (uint32_t)(t >> 2) & 1u, p.timeout_ns) && ok;
+        if (leave()) {
+          aborted = true;
+          break;
+        }
+        if constexpr (!Gm::k16) mask_cur = op_mask[t & 3];
       }
-      ok = mbar_wait_bounded(&my_s[t & 1], (uint32_t)(t >> 1) & 1u, p.timeout_ns) && ok;
-      // quantized: the tile's block mask and FP8 scales, left by the dequantization
-      if constexpr (!Gm::k16) ok = mbar_wait_bounded(&bar_op[t & 3], (uint32_t)(t >> 2) & 1u, p.timeout_ns) && ok;
-      if (leave()) {
-        aborted = true;
-        break;
-      }
-      if constexpr (!Gm::k16) mask_cur = op_mask[t & 3];
       tc::fence_after_sync();
 
       // scores of this row
@@ -717,22 +746,20 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
         // time, and only a row sum that shows a much larger score sends the warp
         // through the general way below, from the same scores. A row that sees
         // nothing gets an argument of 0 x - inf.
-        const int base = (t0 + t) * kN;
-        const bool none = !row_ok || my_hi <= base || my_lo >= base + kN;
-        const bool whole = my_lo <= base && base + kN <= my_hi;
-        bool usual = mask_cur == 0xF && base + kN <= L && __all_sync(kFull, none || (whole && m != -INFINITY));
+        const bool none = t < none_hi || t >= none_lo;
         float cj[4], vr[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          cj[j] = sl2;
-          vr[j] = 1.f;
-          if constexpr (Gm::kFp8) {
-            const float k = tile_sk[(t & 3) * 4 + j], v = tile_sv[(t & 3) * 4 + j];
-            cj[j] *= k;
-            vr[j] = v * rvref;
-            usual = usual && v <= vref;  // the same on every thread
+        for (int j = 0; j < 4; ++j) cj[j] = none ? 0.f : sl2;
+        if constexpr (Gm::kFp8) {
+          const float4 k4 = *reinterpret_cast<const float4*>(tile_sk + (t & 3) * 4);
+          const float4 v4 = *reinterpret_cast<const float4*>(tile_sv + (t & 3) * 4);
+          const float k[4] = {k4.x, k4.y, k4.z, k4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            cj[j] *= k[j];
+            vr[j] = v[j] * rvref;
+            usual = usual && v[j] <= vref;  // the same on every thread
           }
-          if (none) cj[j] = 0.f;
         }
         if (usual) {
           const float nm = none ? -INFINITY : -m;
