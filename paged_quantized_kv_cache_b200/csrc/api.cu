@@ -9,6 +9,7 @@
 
 #include "batch.cuh"
 #include "blocks.cuh"
+#include "cross.cuh"
 #include "decode.cuh"
 #include "prefill.cuh"
 #include "rope.cuh"
@@ -492,12 +493,12 @@ int pqkv_swap_in(void* cache, void* scales, void* outliers_idx, void* outliers_v
                     head_dim, block_ids, num, const_cast<void*>(host_records), err_flag, stream);
 }
 
-// The checks and parameters that the prefill and the cross attention share.
-static int prefill_impl(bool cross, const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
-                        const int32_t* cu_q_lens, const void* cache, const void* scales, const void* outliers_idx,
-                        const void* outliers_val, int kv_dtype, int num_blocks, int num_kv_heads, int head_dim,
-                        const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
-                        const int32_t* ranges, float scale, void* out, int32_t* err_flag, pqkv_stream_t stream) {
+int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
+                                 const int32_t* cu_q_lens, const void* cache, const void* scales,
+                                 const void* outliers_idx, const void* outliers_val, int kv_dtype, int num_blocks,
+                                 int num_kv_heads, int head_dim, const int32_t* block_tables,
+                                 int max_blocks_per_seq, const int32_t* seq_lens, float scale, void* out,
+                                 int32_t* err_flag, pqkv_stream_t stream) {
   if (!is_kv_dtype(kv_dtype) || (q_dtype != PQKV_DTYPE_FP16 && q_dtype != PQKV_DTYPE_BF16)) return PQKV_ERR_ARG;
   if (is_16(kv_dtype) && q_dtype != kv_dtype) return PQKV_ERR_ARG;
   if (batch < 0 || max_q_len < 1 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 ||
@@ -519,14 +520,9 @@ static int prefill_impl(bool cross, const void* q, int q_dtype, int batch, int m
   DeviceInfo di;
   if (!device_info(di)) return PQKV_ERR_CUDA;
   if ((size_t)di.max_smem < prefill_smem_bytes(kv_dtype, head_dim)) return PQKV_ERR_CUDA;
-  const bool few = cross && (int64_t)max_q_len * G <= kFewColumns;
-  // TMA row coordinates and grids fit 32 bits
-  if ((few || is_16(kv_dtype)) && (int64_t)num_blocks * num_kv_heads * 32 >= INT32_MAX) return PQKV_ERR_ARG;
-  if (cross && (int64_t)batch * num_kv_heads >= INT32_MAX / 16) return PQKV_ERR_ARG;
   CUtensorMap tmap;
   std::memset(&tmap, 0, sizeof(tmap));
-  if (few && !cached_cache_map(&tmap, cache, kv_dtype, num_blocks, num_kv_heads, head_dim)) return PQKV_ERR_CUDA;
-  if (!few && is_16(kv_dtype) && !make_prefill_map(&tmap, cache, kv_dtype, num_blocks, num_kv_heads, head_dim))
+  if (is_16(kv_dtype) && !make_prefill_map(&tmap, cache, kv_dtype, num_blocks, num_kv_heads, head_dim))
     return PQKV_ERR_CUDA;
   PrefillParams p;
   p.q = q;
@@ -549,35 +545,9 @@ static int prefill_impl(bool cross, const void* q, int q_dtype, int batch, int m
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = g_decode_wait_ns.load();
   p.drain_ns = kWaitLimitNs;
-  p.ranges = ranges;
-  p.max_q = max_q_len;
-  p.splits = 1;
-  p.q_and = 0xFFFFFFFFu;
-  p.q_xor = 0;
-  if (cross && !few && scale < 0.f) {
-    p.q_xor = 0x80008000u;
-    p.scale_log2 = -p.scale_log2;
-  } else if (cross && !few && scale == 0.f) {
-    p.q_and = 0;
-    p.scale_log2 = 1.f;
-  }
-  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const bool q_bf16 = q_dtype == PQKV_DTYPE_BF16;
-  const cudaError_t e = few     ? launch_cross_few(kv_dtype, head_dim, q_bf16, tmap, p, di.sms, st)
-                        : cross ? launch_cross(kv_dtype, head_dim, q_bf16, tmap, p, di.sms, st)
-                                : launch_prefill(kv_dtype, head_dim, q_bf16, tmap, p, st);
+  const cudaError_t e = launch_prefill(kv_dtype, head_dim, q_dtype == PQKV_DTYPE_BF16, tmap, p,
+                                       reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
-}
-
-int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
-                                 const int32_t* cu_q_lens, const void* cache, const void* scales,
-                                 const void* outliers_idx, const void* outliers_val, int kv_dtype, int num_blocks,
-                                 int num_kv_heads, int head_dim, const int32_t* block_tables,
-                                 int max_blocks_per_seq, const int32_t* seq_lens, float scale, void* out,
-                                 int32_t* err_flag, pqkv_stream_t stream) {
-  return prefill_impl(false, q, q_dtype, batch, max_q_len, num_q_heads, cu_q_lens, cache, scales, outliers_idx,
-                      outliers_val, kv_dtype, num_blocks, num_kv_heads, head_dim, block_tables, max_blocks_per_seq,
-                      seq_lens, nullptr, scale, out, err_flag, stream);
 }
 
 int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
@@ -586,10 +556,65 @@ int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_
                                int num_kv_heads, int head_dim, const int32_t* block_tables, int max_blocks_per_seq,
                                const int32_t* kv_lens, const int32_t* kv_ranges, float scale, void* out,
                                int32_t* err_flag, pqkv_stream_t stream) {
-  if ((reinterpret_cast<uintptr_t>(kv_ranges) & 7u) != 0 || !std::isfinite(scale)) return PQKV_ERR_ARG;
-  return prefill_impl(true, q, q_dtype, batch, max_q_len, num_q_heads, cu_q_lens, cache, scales, outliers_idx,
-                      outliers_val, kv_dtype, num_blocks, num_kv_heads, head_dim, block_tables, max_blocks_per_seq,
-                      kv_lens, kv_ranges, scale, out, err_flag, stream);
+  if (!is_kv_dtype(kv_dtype) || (q_dtype != PQKV_DTYPE_FP16 && q_dtype != PQKV_DTYPE_BF16)) return PQKV_ERR_ARG;
+  if (is_16(kv_dtype) && q_dtype != kv_dtype) return PQKV_ERR_ARG;
+  if (batch < 0 || max_q_len < 1 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 ||
+      max_blocks_per_seq < 1 || max_blocks_per_seq > INT32_MAX / PQKV_BLOCK_SIZE ||
+      (head_dim != 64 && head_dim != 128))
+    return PQKV_ERR_ARG;
+  if (num_q_heads % num_kv_heads != 0) return PQKV_ERR_ARG;
+  const int G = num_q_heads / num_kv_heads;
+  if (128 % G != 0 || num_kv_heads > 65535 || !std::isfinite(scale)) return PQKV_ERR_ARG;
+  const bool few = (int64_t)max_q_len * G <= kFewColumns;
+  const int64_t tiles = ((int64_t)max_q_len * G + 127) / 128;
+  // grids and TMA row coordinates fit 32 bits
+  if (tiles * batch > INT32_MAX || (int64_t)batch * num_kv_heads >= INT32_MAX / 16) return PQKV_ERR_ARG;
+  if ((few || is_16(kv_dtype)) && (int64_t)num_blocks * num_kv_heads * 32 >= INT32_MAX) return PQKV_ERR_ARG;
+  if (batch == 0) return PQKV_OK;
+  if (!q || !cu_q_lens || !cache || !block_tables || !kv_lens || !out || !err_flag) return PQKV_ERR_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(cache) || (reinterpret_cast<uintptr_t>(kv_ranges) & 7u) != 0)
+    return PQKV_ERR_ARG;
+  if (!is_16(kv_dtype) && (!scales || !aligned16(scales))) return PQKV_ERR_ARG;
+  if (kv_dtype == PQKV_DTYPE_FP4_E2M1 &&
+      (!outliers_idx || !outliers_val || !aligned16(outliers_idx) || !aligned16(outliers_val)))
+    return PQKV_ERR_ARG;
+  DeviceInfo di;
+  if (!device_info(di)) return PQKV_ERR_CUDA;
+  if (!few && (size_t)di.max_smem < cross_smem_bytes(kv_dtype, head_dim)) return PQKV_ERR_CUDA;
+  CUtensorMap tmap;
+  std::memset(&tmap, 0, sizeof(tmap));
+  if (few ? !cached_cache_map(&tmap, cache, kv_dtype, num_blocks, num_kv_heads, head_dim)
+          : is_16(kv_dtype) && !make_prefill_map(&tmap, cache, kv_dtype, num_blocks, num_kv_heads, head_dim))
+    return PQKV_ERR_CUDA;
+  CrossParams p;
+  p.q = q;
+  p.out = out;
+  p.cache = static_cast<const uint8_t*>(cache);
+  p.scales = static_cast<const uint8_t*>(scales);
+  p.oidx = static_cast<const uint8_t*>(outliers_idx);
+  p.oval = static_cast<const uint8_t*>(outliers_val);
+  p.cu_q = cu_q_lens;
+  p.kv_lens = kv_lens;
+  p.block_tables = block_tables;
+  p.ranges = kv_ranges;
+  p.err = err_flag;
+  p.B = batch;
+  p.Hq = num_q_heads;
+  p.Hkv = num_kv_heads;
+  p.G = G;
+  p.nb = num_blocks;
+  p.maxblk = max_blocks_per_seq;
+  p.max_q = max_q_len;
+  p.tiles_per_seq = (int)tiles;
+  p.splits = 1;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.timeout_ns = g_decode_wait_ns.load();
+  p.drain_ns = kWaitLimitNs;
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool q_bf16 = q_dtype == PQKV_DTYPE_BF16;
+  const cudaError_t e = few ? launch_cross_few(kv_dtype, head_dim, q_bf16, tmap, p, di.sms, st)
+                            : launch_cross(kv_dtype, head_dim, q_bf16, tmap, p, di.sms, st);
+  return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
 }
 
 int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch, const int32_t* new_block_ids,

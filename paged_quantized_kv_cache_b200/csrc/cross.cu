@@ -1,25 +1,921 @@
 // cross.cu -- attention of decoder tokens to an encoder's cached states, of a
-// length of their own ("vLLM" glossary, "PagedAttention": K/V through the block
-// table, one copy shared by every sequence that reads it).
+// length of their own, on the sm_100a tensor cores (tcgen05, accumulators in
+// tensor memory).
 //
-// The kernel is the prefill's (prefill_kernel.cuh) with CROSS:
-//  - a row sees positions [lo, hi) of [0, L) instead of [0, its own]: the whole
-//    of the states, or the token's range. A CTA walks the tiles between the
-//    first and the last position that any of its rows sees, and masks only tiles
-//    that some row of a warp does not see whole.
-//  - few query rows. Warpgroups and warps without rows take no part (a decode
-//    step has G rows of the 256), and the KV range of a tile pair is split over
-//    a cluster of up to 8 CTAs whose partial O, m and l are joined through
-//    distributed shared memory: no workspace, no second launch, no order that
-//    depends on timing.
-#include "prefill_kernel.cuh"
+// "vLLM" glossary, "PagedAttention": K/V through the block table, one copy read
+// by every sequence whose table names it. out = softmax(scale q K^T) V over the
+// positions [lo, hi) of [0, L) that the token sees: all of them, or its range.
+//
+// Work decomposition. A row is (query token, query head of the GQA group); a CTA
+// takes up to two tiles of 128 rows of one (sequence, KV head) and the KV tiles
+// of 64 positions (4 blocks) between the first and the last position that any
+// of its rows sees. With one row tile both halves of the CTA take it, one the
+// even KV tiles and one the odd ("dup"), and a small grid splits the KV tiles
+// over a cluster of up to 8 CTAs; the parts' O, m and l are joined through
+// (distributed) shared memory. No workspace, one launch, no order that depends
+// on timing. Warps have one role each, handing over by mbarriers:
+//   compute warps: H groups of 4 per row tile, which take its KV tiles in turn,
+//     one row per thread (its S, P and O lie in tensor-memory lane r of the row
+//     tile's 256 columns): online softmax;
+//   producer warps: refill rings of KV tiles, for 16-bit caches one ring of K
+//     tiles (free once S is computed) and one of V tiles, each with a warp;
+//   for quantized caches 8 dequantization warps: raw codes -> f16 operands;
+//   an MMA warp per row tile: S(u) = Q K^T into one of two S buffers, PV(u) from
+//     P(u) in tensor memory over the columns of S(u), then S(u + 2).
+//
+// Softmax. In the usual tile every row of a warp sees all of it or nothing and
+// has a max from earlier tiles. That max then stays: exponents are taken against
+// it while the scores arrive, 16 columns (a cache block) at a time, without a
+// max of the tile, and only a row sum that shows a much larger score (f16 P:
+// 2^15, bf16 P, which has the range of fp32: 2^60) takes the tile again the
+// general way: masks, max, rescaling of O and l. With H = 2 the warps of a row's
+// two groups hand P over in the order of the tiles (a turn per 32 rows): the
+// max is shared, and a warp whose turn comes after the max was moved takes its
+// tile again.
+//
+// P is rounded once to the operand type (f16 2^-11, bf16 2^-8 of its value: the
+// weights of a mean, whose 16-bit result is rounded as much itself); P_hi + P_lo
+// as in the prefill costs half as many products again (16 sequences of 300-512
+// tokens over 3203-6404 bf16 states: 697 against 616 us).
+//
+// FP8 scales stay out of the operands: the K scale of a block multiplies its
+// scores, the V scale P relative to the largest so far (O is kept in units of
+// it). FP4 operands are exact in f16 (E2M1 x E4M3, fp16 outlier values).
+#include <atomic>
+#include <cfloat>
+#include <climits>
+
+#include "attn_math.cuh"
+#include "cluster.cuh"
+#include "cross.cuh"
+#include "tcgen05.cuh"
 
 namespace pqkv {
 
 namespace {
 
-// CTAs per tile pair: doubled while the doubled grid still fits the GPU at one
-// CTA per SM and every CTA keeps a tile.
+constexpr int kM = 128;        // rows of a tile
+constexpr int kN = 64;         // KV positions of a tile (4 blocks)
+constexpr int kMaxSplits = 8;  // CTAs of a cluster (the portable limit)
+constexpr float kLazy = 8.f;   // the general way moves a row's max only when it grows by more (log2 units)
+constexpr unsigned kFull = 0xFFFFFFFFu;
+
+template <int KVF, int D>
+struct CrossGeom {
+  static constexpr bool k16 = (KVF == PQKV_DTYPE_FP16 || KVF == PQKV_DTYPE_BF16);
+  static constexpr bool kFp8 = (KVF == PQKV_DTYPE_FP8_E4M3 || KVF == PQKV_DTYPE_FP8_E5M2);
+  static constexpr bool kFp4 = (KVF == PQKV_DTYPE_FP4_E2M1);
+  // Groups of compute warps per row tile. A tile costs a warp about as long in
+  // latencies (waits, tensor memory, votes, hand-overs) as in exponents, so 16-bit
+  // caches alternate two groups; quantized caches give those warps' registers to
+  // the dequantization, which bounds them.
+  static constexpr int H = k16 ? 2 : 1;
+  static constexpr int kComputeWarps = 8 * H;
+  static constexpr int kProducer = kComputeWarps;     // warp roles, in order
+  static constexpr int kProducers = k16 ? 2 : 1;      // K and V, or raw tiles
+  static constexpr int kMma = kProducer + kProducers; // two of them
+  static constexpr int kDeq = kMma + 2;
+  static constexpr int kDeqWarps = k16 ? 0 : 8;
+  static constexpr int kDeqThreads = 32 * kDeqWarps;
+  static constexpr int kThreads = 32 * (kDeq + kDeqWarps);
+  static constexpr int NB = D / 64;                   // 128-byte boxes per operand row
+  static constexpr int kQBytes = NB * kM * 128;       // Q operand of a row tile [box][128 rows][128 B]
+  static constexpr int kOpBytes = NB * kN * 128;      // one K or V operand tile [box][64 rows][128 B]
+  static constexpr int kRawTile = 32 * row_bytes(KVF, D);  // one block's K|V codes
+  static constexpr int kScaleBytes = kFp8 ? 16 : (kFp4 ? 2 * 16 * (D / 16) : 0);
+  static constexpr int kValBytes = kFp4 ? 2 * 16 * 4 * 2 : 0;
+  static constexpr int kIdxBytes = kFp4 ? 16 : 0;
+  static constexpr int kSide = kScaleBytes + kValBytes + kIdxBytes;
+  static constexpr int kStages = 4;                   // KV tiles in flight; 16-bit dup: one more, in the free Q tile
+  static constexpr int kMaxStages = kStages + 1;
+  static constexpr int kRawStage = k16 ? 2 * kOpBytes : 4 * (kRawTile + kSide);
+  static constexpr int kStageBytes = (kRawStage + 1023) / 1024 * 1024;
+  static_assert(!k16 || kStageBytes == kQBytes, "a KV tile fits a Q tile's place");
+  static constexpr int kKops = k16 ? 0 : 2;           // dequantized K tiles
+  static constexpr int kVops = k16 ? 0 : 3;           // dequantized V tiles
+  static constexpr int kMasks = 16;                   // block masks of KV tiles t % 16
+  static constexpr int oQ = 0;
+  static constexpr int oStage = oQ + 2 * kQBytes;
+  static constexpr int oKop = oStage + kStages * kStageBytes;
+  static constexpr int oVop = oKop + kKops * kOpBytes;
+  static constexpr int oMisc = oVop + kVops * kOpBytes;
+  static constexpr int kBars = 4 * kMaxStages + 12 + 4 + 2 + 3 + 8 + 2;
+  static constexpr int oScales = oMisc + (kBars * 8 + 15) / 16 * 16;  // FP8 scales of tile t % 4: K [4][4], V [4][4]
+  static constexpr int oWords = oScales + 128;
+  static constexpr int kWords = kMasks + kMaxStages + 1 + 2 + 8 + 2 + 1;
+  static constexpr int oRows = oWords + (kWords * 4 + 15) / 16 * 16;  // H = 2: max, and sum of each group, of every row
+  static constexpr int kSmem = oRows + (H == 2 ? 3 * 2 * kM * 4 : 0) + 1024;  // + alignment slack
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+  static_assert(2 * kM * (D * 4 + 8) <= oMisc, "partial O, m and l over the queries, stages and operands");
+};
+
+template <int N>
+__device__ __forceinline__ void deq_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+
+// And-reduction over the `n` threads (a multiple of 32) of named barrier `id`.
+__device__ __forceinline__ bool bar_all(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// Exponents of a row's 64 scores (at t_s) in log2 units, x cj + nm: P, times
+// vr, goes to pk as pairs of the operand type, its sum (before vr) is returned.
+// kMasked: columns outside `cols` (a bit each) give 0.
+template <bool kMasked, bool kFp8, bool kBf16>
+__device__ __forceinline__ float exponents(uint32_t t_s, float nm, const float (&cj)[4], const float (&vr)[4],
+                                           uint64_t cols, uint32_t (&pk)[32]) {
+  float ra[2] = {0.f, 0.f}, rb[2] = {0.f, 0.f};
+  uint32_t x[2][16];
+  tc::tmem_ld16_start(t_s, x[0]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    tc::tmem_ld_wait(x[j & 1]);
+    if (j < 3) tc::tmem_ld16_start(t_s + 16 * (j + 1), x[(j + 1) & 1]);
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      float ya, yb;
+      fma2(ya, yb, __uint_as_float(x[j & 1][c]), __uint_as_float(x[j & 1][c + 1]), cj[j], cj[j], nm, nm);
+      if constexpr (kMasked) {
+        if (!((cols >> (16 * j + c)) & 1)) ya = -INFINITY;
+        if (!((cols >> (16 * j + c + 1)) & 1)) yb = -INFINITY;
+      }
+      float pa = ex2(ya), pb = ex2(yb);
+      const int i = (c >> 1) & 1;
+      add2(ra[i], rb[i], ra[i], rb[i], pa, pb);
+      if constexpr (kFp8) mul2(pa, pb, pa, pb, vr[j], vr[j]);
+      pk[8 * j + (c >> 1)] = pack_f32x2(pa, pb, kBf16);
+    }
+  }
+  return (ra[0] + ra[1]) + (rb[0] + rb[1]);
+}
+
+// The largest of a row's scores x cj (kMasked: of those in `cols`).
+template <bool kMasked>
+__device__ __forceinline__ float largest(uint32_t t_s, const float (&cj)[4], uint64_t cols) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t x[2][16];
+  tc::tmem_ld16_start(t_s, x[0]);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    tc::tmem_ld_wait(x[j & 1]);
+    if (j < 3) tc::tmem_ld16_start(t_s + 16 * (j + 1), x[(j + 1) & 1]);
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (!kMasked || ((cols >> (16 * j + c)) & 1)) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[j & 1][c]) * cj[j]);
+  }
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
+template <int KVF, int D, bool QBF16>
+__global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
+    paged_cross_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ CrossParams p) {
+  using Gm = CrossGeom<KVF, D>;
+  constexpr int H = Gm::H;
+  constexpr bool kBfMma = (KVF == PQKV_DTYPE_BF16);  // operand type: bf16 for a bf16 cache, else f16
+  constexpr uint32_t kIdescS = tc::f16_idesc(kBfMma, kM, kN, false);
+  constexpr uint32_t kIdescPV = tc::f16_idesc(kBfMma, kM, D, true);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* sKop = smem + Gm::oKop;
+  uint8_t* sVop = smem + Gm::oVop;
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + Gm::oMisc);  // [kMaxStages] tile (16-bit: its K) landed
+  uint64_t* bar_empty = bar_full + Gm::kMaxStages;                      // [kMaxStages] its stage free again
+  uint64_t* bar_vfull = bar_empty + Gm::kMaxStages;                     // 16-bit: the same for V
+  uint64_t* bar_vempty = bar_vfull + Gm::kMaxStages;
+  uint64_t* bar_s = bar_vempty + Gm::kMaxStages;  // [2][2] row tile w's S(u) computed (buffer u % 2)
+  uint64_t* bar_p = bar_s + 4;                   // [2][2] its P(u) in tensor memory (one arrival per warp)
+  uint64_t* bar_pv = bar_p + 4;                  // [2][2] its PV(u) computed
+  uint64_t* bar_op = bar_pv + 4;                 // [4] quantized: operands, mask and scales of tile t ready
+  uint64_t* bar_kfree = bar_op + 4;              // [2] quantized: every S(t) done (kop[t % 2])
+  uint64_t* bar_vfree = bar_kfree + 2;           // [3] quantized: every PV(t) done (vop[t % 3])
+  uint64_t* bar_turn = bar_vfree + 3;            // [2][4] H = 2: tile u of these 32 rows handed over (phase u)
+  uint64_t* bar_drain = bar_turn + 8;            // [2] every product an MMA warp issued has completed
+  float* tile_sk = reinterpret_cast<float*>(smem + Gm::oScales);  // [4][4] FP8 K scales of tile t % 4
+  float* tile_sv = tile_sk + 16;                                  // [4][4] FP8 V scales
+  volatile int* tile_mask = reinterpret_cast<volatile int*>(smem + Gm::oWords);  // [kMasks] blocks of tile t that hold data
+  volatile int* stage_mask = tile_mask + Gm::kMasks;  // [kMaxStages] quantized: the same, of a raw stage
+  volatile int* abort_flag = stage_mask + Gm::kMaxStages;
+  volatile int* n_issued = abort_flag + 1;       // [2] tiles that the producers started
+  volatile int* row_moves = n_issued + 2;        // [2][4] H = 2: how often the max of these 32 rows was moved
+  int* span = const_cast<int*>(row_moves) + 8;   // [2] positions that rows of the CTA see
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(span + 2);
+  float* row_max = reinterpret_cast<float*>(smem + Gm::oRows);  // [2][128] H = 2
+  float* row_sum = row_max + 2 * kM;                            // [2 groups][2][128] H = 2
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same register for the whole warp
+  const int h = blockIdx.y, rank = blockIdx.z;
+  const int G = p.G, TOK = kM / G;
+  const int ctas = (p.tiles_per_seq + 1) / 2;
+  const int b = blockIdx.x / ctas, mt0 = 2 * (int)(blockIdx.x % ctas);  // first row tile
+  const int q0 = p.cu_q[b], qn = p.cu_q[b + 1] - q0;
+  const int L = p.kv_lens[b];
+  if (mt0 == 0 && h == 0 && rank == 0 && tid == 0 && qn > p.tiles_per_seq * TOK)
+    raise_flag(p.err, PQKV_DEVERR_SEQ_LEN);  // rows past max_q_len are not computed
+  if (qn <= 0 || mt0 * TOK >= qn) return;
+  const bool rejected = L < 0 || L > kBlock * p.maxblk;
+  if (rejected && mt0 == 0 && h == 0 && rank == 0 && tid == 0) raise_flag(p.err, PQKV_DEVERR_SEQ_LEN);
+
+  const int n_rows = min(min(qn - mt0 * TOK, 2 * TOK) * G, min(p.tiles_per_seq - mt0, 2) * kM);
+  // compute warps: half of the CTA (0, 1), group (0 .. H - 1), quarter of the tile's lanes
+  const bool is_compute = warp < Gm::kComputeWarps;
+  const int wg = (warp >> 2) & 1, group = warp >> 3, quad = warp & 3;
+  const int r = 32 * quad + lane;
+  const bool one_tile = n_rows <= kM;
+  const int row = (one_tile ? 0 : wg * kM) + r;           // row of this thread in the CTA's rows
+  const bool row_ok = is_compute && row < n_rows;
+  const int my_token = q0 + mt0 * TOK + (row_ok ? row / G : 0);
+  const size_t orow = ((size_t)my_token * p.Hq + (size_t)h * G + row % G) * D;
+  // warps of half w's row tile that hold rows
+  auto warps_of = [&](int w) { return min(4, (n_rows - (one_tile ? 0 : w * kM) + 31) / 32); };
+
+  // ---- positions that the rows see; the KV tiles of this CTA ----
+  int my_lo = 0, my_hi = 0, lo = 0, hi = rejected ? 0 : L;
+  if (p.ranges && !rejected) {
+    if (tid == 0) {
+      span[0] = L;
+      span[1] = 0;
+    }
+    __syncthreads();
+    if (row_ok) {
+      const int2 r2 = __ldg(reinterpret_cast<const int2*>(p.ranges) + my_token);
+      my_lo = max(r2.x, 0);
+      my_hi = min(r2.y, L);
+    }
+    if (is_compute) {
+      const bool sees = row_ok && my_lo < my_hi;
+      const int a = __reduce_min_sync(kFull, sees ? my_lo : INT_MAX), z = __reduce_max_sync(kFull, sees ? my_hi : 0);
+      if (lane == 0 && z > 0) {
+        atomicMin(&span[0], a);
+        atomicMax(&span[1], z);
+      }
+    }
+    __syncthreads();
+    lo = span[0];
+    hi = span[1];
+  } else if (row_ok) {
+    my_hi = hi;
+  }
+  const int first = lo / kN, tiles = max(0, (hi + kN - 1) / kN - first);
+  if (tiles == 0) {  // the same for every CTA of the cluster: no row sees anything
+    if (row_ok && rank == 0 && group == 0 && (!one_tile || wg == 0)) {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow);
+      for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int share = (tiles + p.splits - 1) / p.splits;
+  const int t0 = first + rank * share;                        // tile 0 of this CTA
+  const int T = max(0, min(share, tiles - rank * share));
+  // one row tile: the halves of the CTA take the KV tiles in turn, half w tiles
+  // w, w + 2, ... (the second half has none if there is one KV tile)
+  const bool dup = one_tile && share > 1;
+  const int pshift = dup ? 1 : 0, par = 1 << pshift;
+  const int consumers = one_tile ? 1 : 2;  // MMA warps that read a KV tile
+  auto tiles_of = [&](int w) { return dup ? (T - w + 1) >> 1 : (one_tile && w > 0 ? 0 : T); };
+  const int32_t* table = p.block_tables + (size_t)b * p.maxblk;
+  const int ns = Gm::k16 && one_tile ? Gm::kMaxStages : Gm::kStages;
+  auto stage_at = [&](int s) -> uint8_t* {
+    return s < Gm::kStages ? smem + Gm::oStage + s * Gm::kStageBytes : smem + Gm::oQ + Gm::kQBytes;
+  };
+  auto stage_of = [&](int t) { return ns == 4 ? t & 3 : t % 5; };
+  auto lap_of = [&](int t) { return (uint32_t)(ns == 4 ? t >> 2 : t / 5) & 1u; };
+
+  // ---- setup: tensor memory, barriers, Q tiles ----
+  if (warp == 0) tc::tmem_alloc(tmem_slot, 512);
+  if (tid == 32 * Gm::kProducer) {
+    if constexpr (Gm::k16) prefetch_tensormap(&tmap);
+    for (int s = 0; s < Gm::kMaxStages; ++s) {
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_empty[s], Gm::k16 ? consumers : 1);  // 16-bit: each MMA warp's commit; else dequantized
+      mbar_init(&bar_vfull[s], 1);
+      mbar_init(&bar_vempty[s], consumers);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar_s[i], 1);
+      mbar_init(&bar_p[i], max(1, warps_of(i >> 1)));
+      mbar_init(&bar_pv[i], 1);
+      mbar_init(&bar_op[i], 1);
+    }
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&bar_turn[i], 1);
+      row_moves[i] = 0;
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&bar_kfree[i], consumers);
+    for (int i = 0; i < 3; ++i) mbar_init(&bar_vfree[i], consumers);
+    for (int i = 0; i < 2; ++i) mbar_init(&bar_drain[i], 1);
+    *abort_flag = 0;
+    n_issued[0] = n_issued[1] = 0;
+    fence_mbar_init();
+  }
+  // softmax scale in log2 units of this thread's row, times 2^e when the row's
+  // bf16 query was scaled by 2^-e before narrowing to f16 (quantized caches)
+  float sl2 = p.scale_log2;
+  if (is_compute) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow);
+    float qmul = 1.f;
+    if constexpr (!Gm::k16 && QBF16) {
+      // the power of two 2^-e that brings the row's largest |q| into
+      // [2^13, 2^14): exact, and far from both ends of the f16 range
+      float mx = 0.f;
+      if (row_ok) {
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = __ldg(src + c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+        }
+      }
+      const int ex = (mx > 0.f && mx <= FLT_MAX) ? ilogbf(mx) - 13 : 0;
+      qmul = ldexpf(1.f, -ex);
+      sl2 = p.scale_log2 * ldexpf(1.f, ex);
+    }
+    if (!one_tile || wg == 0) {
+      // this thread's share of its row of the Q tile, converted to the operand
+      // type, 16-byte chunks swizzled; rows past the end are zeros
+      uint8_t* sQ = smem + Gm::oQ + (one_tile ? 0 : wg) * Gm::kQBytes;
+#pragma unroll 4
+      for (int c = group * (D / 8 / H); c < (group + 1) * (D / 8 / H); ++c) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row_ok) v = __ldg(src + c);
+        if constexpr (!Gm::k16 && QBF16) {
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = to_f16x2(__uint_as_float(w[i] << 16) * qmul, __uint_as_float(w[i] & 0xFFFF0000u) * qmul);
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4*>(sQ + (c >> 3) * (kM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      }
+    }
+  }
+  tc::fence_smem_to_async();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  float m = -INFINITY, l = 0.f, vref = 0.f;  // this row's max, sum (of this thread's tiles), FP8 unit of O
+  bool aborted = false;
+
+  if (warp >= Gm::kProducer && warp < Gm::kMma) {
+    // ================= producers: KV tiles (16-bit: K, and V) into the stage rings =================
+    if (lane == 0) {
+      const int kv = warp - Gm::kProducer;  // 16-bit: 0 = K, 1 = V
+      uint64_t* full = kv ? bar_vfull : bar_full;
+      uint64_t* empty = kv ? bar_vempty : bar_empty;
+      int t = 0;
+      for (; t < T; ++t) {
+        const int s = stage_of(t);
+        if (t >= ns && !mbar_wait_bounded(&empty[s], lap_of(t) ^ 1u, p.timeout_ns)) break;
+        if (*abort_flag) break;
+        uint8_t* st = stage_at(s);
+        int ids[4];
+        int mask = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int blk = 4 * (t0 + t) + j;
+          ids[j] = blk * kBlock < hi ? __ldg(table + blk) : -1;
+          if (ids[j] >= 0 && ids[j] < p.nb) mask |= 1 << j;
+          else if (blk * kBlock < hi) raise_flag(p.err, PQKV_DEVERR_BLOCK_ID);
+        }
+        // published to the consumers by the stage's barrier
+        if (!Gm::k16) stage_mask[s] = mask;
+        else if (kv == 0) tile_mask[t % Gm::kMasks] = mask;
+        constexpr uint32_t kBytes = Gm::k16 ? (uint32_t)Gm::NB * kBlock * 128u : (uint32_t)(Gm::kRawTile + Gm::kSide);
+        mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(mask) * kBytes);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!((mask >> j) & 1)) continue;
+          const size_t pair = (size_t)ids[j] * p.Hkv + h;
+          if constexpr (Gm::k16) {
+#pragma unroll
+            for (int bx = 0; bx < Gm::NB; ++bx)
+              tma_load_2d(st + kv * Gm::kOpBytes + bx * kN * 128 + j * kBlock * 128, &tmap, bx * 64,
+                          (int)pair * 32 + 16 * kv, &full[s]);
+          } else {
+            bulk_load(st + j * Gm::kRawTile, p.cache + pair * Gm::kRawTile, Gm::kRawTile, &full[s]);
+            uint8_t* side = st + 4 * Gm::kRawTile + j * Gm::kSide;
+            if constexpr (Gm::kFp8) {
+              bulk_load(side, p.scales + pair * 16, 16, &full[s]);
+            } else {
+              bulk_load(side, p.scales + pair * Gm::kScaleBytes, Gm::kScaleBytes, &full[s]);
+              bulk_load(side + Gm::kScaleBytes, p.oval + pair * Gm::kValBytes, Gm::kValBytes, &full[s]);
+              bulk_load(side + Gm::kScaleBytes + Gm::kValBytes, p.oidx + pair * 16, 16, &full[s]);
+            }
+          }
+        }
+      }
+      n_issued[kv] = t;
+    }
+  } else if (warp >= Gm::kMma && warp < Gm::kMma + 2) {
+    // ================= MMA warp of half w: its products, KV tiles t = w0 + u par =================
+    // Order: PV(u) once P(u) is in tensor memory, then S(u + 2) into the buffer
+    // that P(u) occupied, once PV(u) has read it. S(0) and S(1) come first, so
+    // the half finds the scores of its next tile computed.
+    // The whole warp walks the tiles, so that addresses stay in uniform
+    // registers; one thread of it issues.
+    const int w = warp - Gm::kMma, w0 = dup ? w : 0, U = tiles_of(w);
+    bool good = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      good = __all_sync(kFull, mbar_test_wait(bar, parity) || mbar_wait_bounded(bar, parity, p.timeout_ns)) && good;
+    };
+    // K (with it, quantized, V) of tile t is there
+    auto wait_k = [&](int t) {
+      if constexpr (Gm::k16) wait(&bar_full[stage_of(t)], lap_of(t));
+      else wait(&bar_op[t & 3], (uint32_t)(t >> 2) & 1u);
+    };
+    const uint32_t base = smem_u32(smem);
+    const uint32_t qa = base + Gm::oQ + (one_tile ? 0 : w) * Gm::kQBytes;
+    const bool issuer = tc::elect_one();
+    auto stage_addr = [&](int s) -> uint32_t {
+      return base + (s < Gm::kStages ? Gm::oStage + s * Gm::kStageBytes : Gm::oQ + Gm::kQBytes);
+    };
+    const uint64_t q_desc = tc::sw128_desc(qa, 16, 1024);
+    auto issue_s = [&](int u) {
+      const int t = w0 + (u << pshift);
+      tc::fence_after_sync();
+      const uint32_t d = tmem + 256u * w + D + 64 * (u & 1);
+      const uint32_t ka = Gm::k16 ? stage_addr(stage_of(t)) : base + Gm::oKop + (t & 1) * Gm::kOpBytes;
+      const uint64_t k_desc = tc::sw128_desc(ka, 16, 1024);
+      if (issuer) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)  // addresses in units of 16 bytes; no field overflows (shared memory)
+          tc::mma_ss(d, q_desc + (kk >> 2) * (kM * 8) + (kk & 3) * 2, k_desc + (kk >> 2) * (kN * 8) + (kk & 3) * 2,
+                     kIdescS, kk > 0);
+        tc::commit(&bar_s[2 * w + (u & 1)]);
+        tc::commit(Gm::k16 ? &bar_empty[stage_of(t)] : &bar_kfree[t & 1]);  // K may be refilled
+      }
+    };
+    auto issue_pv = [&](int u) {
+      const int t = w0 + (u << pshift);
+      tc::fence_after_sync();
+      const uint32_t va = Gm::k16 ? stage_addr(stage_of(t)) + Gm::kOpBytes : base + Gm::oVop + (t % 3) * Gm::kOpBytes;
+      const uint64_t v_desc = tc::sw128_desc(va, kN * 128, 1024);
+      const uint32_t o = tmem + 256u * w, pa = o + D + 64 * (u & 1);
+      if (issuer) {
+#pragma unroll
+        for (int kk = 0; kk < kN / 16; ++kk)
+          tc::mma_ts(o, pa + kk * 8, v_desc + kk * 128, kIdescPV, u > 0 || kk > 0);
+        tc::commit(&bar_pv[2 * w + (u & 1)]);
+        tc::commit(Gm::k16 ? &bar_vempty[stage_of(t)] : &bar_vfree[t % 3]);  // V may be refilled
+      }
+    };
+    for (int u = 0; u < min(2, U) && good; ++u) {
+      wait_k(w0 + (u << pshift));
+      if (good) issue_s(u);
+    }
+    for (int u = 0; u < U && good; ++u) {
+      const int t = w0 + (u << pshift);
+      wait(&bar_p[2 * w + (u & 1)], (uint32_t)(u >> 1) & 1u);
+      if constexpr (Gm::k16) wait(&bar_vfull[stage_of(t)], lap_of(t));
+      if (!good) break;
+      issue_pv(u);
+      if (u + 2 < U) {
+        wait_k(t + (2 << pshift));
+        wait(&bar_pv[2 * w + (u & 1)], (uint32_t)(u >> 1) & 1u);
+        if (good) issue_s(u + 2);
+      }
+    }
+    if (!good && lane == 0) {
+      *abort_flag = 1;
+      raise_flag(p.err, PQKV_DEVERR_TIMEOUT);
+    }
+    // every product issued completes before tensor memory is released
+    if (issuer) tc::commit(&bar_drain[w]);
+    if (!mbar_wait_bounded(&bar_drain[w], 0, p.drain_ns) && lane == 0) raise_flag(p.err, PQKV_DEVERR_DRAIN);
+  } else if (!is_compute) {
+    // ================= dequantization warps (quantized caches) =================
+    // Tile t: raw codes landed, the operand buffers free again (every S(t - 2)
+    // read kop[t % 2], every PV(t - 3) vop[t % 3]), then the codes become f16
+    // operands; bar_op[t % 4] hands them, the tile's block mask and FP8 scales
+    // over, and the raw stage goes back to the producer. The warps leave
+    // together, at a consensus.
+    if constexpr (!Gm::k16) {
+      const int dq = tid - 32 * Gm::kDeq;
+      bool ok = true;
+      for (int t = 0; t < T; ++t) {
+        const int s = stage_of(t);
+        ok = mbar_wait_bounded(&bar_full[s], lap_of(t), p.timeout_ns) && ok;
+        if (t >= 2) ok = mbar_wait_bounded(&bar_kfree[t & 1], (uint32_t)((t >> 1) - 1) & 1u, p.timeout_ns) && ok;
+        if (t >= 3) ok = mbar_wait_bounded(&bar_vfree[t % 3], (uint32_t)((t / 3) - 1) & 1u, p.timeout_ns) && ok;
+        ok = bar_all(1, Gm::kDeqThreads, ok);
+        if (!ok) break;
+        const int mask = stage_mask[s];
+        const int base = (t0 + t) * kN;
+        uint8_t* st = stage_at(s);
+        uint8_t* kop = sKop + (t & 1) * Gm::kOpBytes;
+        uint8_t* vop = sVop + (t % 3) * Gm::kOpBytes;
+        constexpr int CPR = D / 8;  // 16-byte operand chunks per row
+        constexpr int kRounds = kN * CPR / Gm::kDeqThreads;  // a compile-time count: fully unrolled
+        static_assert(kN * CPR % Gm::kDeqThreads == 0, "whole rounds");
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+          const int u = dq + k * Gm::kDeqThreads;
+          const int rr = u / CPR, c = u % CPR, j = rr >> 4, tr = rr & 15;
+          uint32_t kf[4] = {0, 0, 0, 0}, vf[4] = {0, 0, 0, 0};
+          if (((mask >> j) & 1) && base + rr < L) {
+            const uint8_t* tile = st + j * Gm::kRawTile;
+            if constexpr (Gm::kFp8) {
+              const uint2 kc = *reinterpret_cast<const uint2*>(tile + tr * D + 8 * c);
+              const uint2 vc = *reinterpret_cast<const uint2*>(tile + (16 + tr) * D + 8 * c);
+              kf[0] = dec_fp8x2<KVF>(kc.x);
+              kf[1] = dec_fp8x2<KVF>(kc.x >> 16);
+              kf[2] = dec_fp8x2<KVF>(kc.y);
+              kf[3] = dec_fp8x2<KVF>(kc.y >> 16);
+              vf[0] = dec_fp8x2<KVF>(vc.x);
+              vf[1] = dec_fp8x2<KVF>(vc.x >> 16);
+              vf[2] = dec_fp8x2<KVF>(vc.y);
+              vf[3] = dec_fp8x2<KVF>(vc.y >> 16);
+            } else {
+              const uint8_t* side = st + 4 * Gm::kRawTile + j * Gm::kSide;
+              constexpr int SPR = D / 16;  // scale bytes per token row
+              // K: row tr, channels 8c..8c+7 = 4 bytes, channel 2i in the low nibble
+              dec_e2m1x8(*reinterpret_cast<const uint32_t*>(tile + tr * (D / 2) + 4 * c), kf);
+              // V: token-pair rows; this token's nibble of channels 8c..8c+7
+              const int hh = (8 * c) / (D / 2);
+              const int pr = tr < 8 ? (tr & ~1) : (((tr - 8) & ~1) + 1);
+              const uint2 wv =
+                  *reinterpret_cast<const uint2*>(tile + (16 + 8 * hh + pr) * (D / 2) + (8 * c) % (D / 2));
+              const uint32_t x0 = ((tr & 1) ? (wv.x >> 4) : wv.x) & 0x0F0F0F0Fu;
+              const uint32_t x1 = ((tr & 1) ? (wv.y >> 4) : wv.y) & 0x0F0F0F0Fu;
+              dec_e2m1x8(prmt(x0 | (x0 >> 4), x1 | (x1 >> 4), 0x6420u), vf);
+              const __half2 sk = scale2(side[tr * SPR + (c >> 1)]);
+              const __half2 sv = scale2(side[16 * SPR + tr * SPR + (c >> 1)]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                kf[i] = hmul2u(kf[i], sk);
+                vf[i] = hmul2u(vf[i], sv);
+              }
+            }
+          }
+          const uint32_t off = (c >> 3) * (kN * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+          *reinterpret_cast<uint4*>(kop + off) = make_uint4(kf[0], kf[1], kf[2], kf[3]);
+          *reinterpret_cast<uint4*>(vop + off) = make_uint4(vf[0], vf[1], vf[2], vf[3]);
+        }
+        if constexpr (Gm::kFp4) {
+          // outlier channels (their codes are 0): write the fp16 values over them;
+          // item = (block j, K|V, slot, eighth of the tokens)
+          deq_sync<Gm::kDeqThreads>();
+          static_assert(Gm::kDeqThreads == 256, "an item per thread");
+          const int j = dq >> 6, kv = (dq >> 5) & 1, slot = (dq >> 3) & 3, eighth = dq & 7;
+          if ((mask >> j) & 1) {
+            const uint8_t* side = st + 4 * Gm::kRawTile + j * Gm::kSide;
+            const int ch = side[Gm::kScaleBytes + Gm::kValBytes + 8 * kv + slot];
+            if (ch < D) {
+              const uint16_t* val = reinterpret_cast<const uint16_t*>(side + Gm::kScaleBytes) + kv * 64;
+              uint8_t* op = kv ? vop : kop;
+              const int c = ch >> 3;
+#pragma unroll
+              for (int q4 = 0; q4 < 2; ++q4) {
+                const int tr = 2 * eighth + q4, rr = 16 * j + tr;
+                if (base + rr < L)
+                  *reinterpret_cast<uint16_t*>(op + (c >> 3) * (kN * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4) +
+                                               (ch & 7) * 2) = val[tr * 4 + slot];
+              }
+            }
+          }
+        }
+        if constexpr (Gm::kFp8) {
+          if (dq < 4) {
+            const bool okb = (mask >> dq) & 1;
+            const float* sc = reinterpret_cast<const float*>(st + 4 * Gm::kRawTile + dq * Gm::kSide);
+            tile_sk[(t & 3) * 4 + dq] = okb ? sc[0] : 0.f;
+            tile_sv[(t & 3) * 4 + dq] = okb ? sc[1] : 0.f;
+          }
+        }
+        if (dq == 0) tile_mask[t % Gm::kMasks] = mask;
+        tc::fence_smem_to_async();
+        deq_sync<Gm::kDeqThreads>();  // every thread's part is written
+        if (dq == 0) {
+          mbar_arrive(&bar_empty[s]);  // a raw stage is free as soon as it is dequantized
+          mbar_arrive(&bar_op[t & 3]);
+        }
+      }
+      if (!ok && dq == 0) {
+        *abort_flag = 1;
+        raise_flag(p.err, PQKV_DEVERR_TIMEOUT);
+      }
+    }
+  } else if (quad < warps_of(wg)) {
+    // ================= compute warps: row r of half wg, its tiles u = group, group + H, ... =================
+    const uint32_t t_row = tmem + 256u * wg + ((uint32_t)(32 * quad) << 16);
+    uint64_t* my_s = bar_s + 2 * wg;
+    uint64_t* my_p = bar_p + 2 * wg;
+    uint64_t* my_pv = bar_pv + 2 * wg;
+    uint64_t* my_turn = bar_turn + 4 * wg + quad;
+    const int w0 = dup ? wg : 0, U = tiles_of(wg);
+    bool ok = true;      // no wait of this thread has timed out
+    float rvref = 0.f;   // FP8: 1 / vref (0 while vref is 0)
+    int moves = 0;       // H = 2: moves of the max that this warp has followed
+    // tiles [whole_lo, whole_hi) of the CTA lie inside this row's range, tiles
+    // below none_hi and from none_lo on outside it; those below t_full end
+    // inside the states
+    int whole_lo = 0, whole_hi = 0, none_hi = INT_MAX, none_lo = 0;
+    const int t_full = L / kN - t0;
+    if (row_ok && my_lo < my_hi) {
+      whole_lo = (my_lo + kN - 1) / kN - t0;
+      whole_hi = my_hi / kN - t0;
+      none_hi = my_lo / kN - t0;
+      none_lo = (my_hi + kN - 1) / kN - t0;
+    }
+    constexpr float kMost = kBfMma ? 0x1p60f : 0x1p15f;  // largest row sum of a tile: P fits its type
+    // the max was moved by the row's other group: l follows
+    auto follow = [&]() {
+      const float to = row_max[wg * kM + r];
+      l *= m == to ? 1.f : ex2(m - to);  // 0 when m was -inf (and l 0)
+      m = to;
+    };
+
+    for (int u = group; u < U; u += H) {
+      const int t = w0 + (u << pshift);
+      const uint32_t t_s = t_row + D + 64 * (u & 1);
+      ok = (mbar_test_wait(&my_s[u & 1], (uint32_t)(u >> 1) & 1u) ||
+            mbar_wait_bounded(&my_s[u & 1], (uint32_t)(u >> 1) & 1u, p.timeout_ns)) && ok;
+      // S(u) done: its MMA warp saw the tile's operands, mask and scales, so they are visible here too
+      const int mask = tile_mask[t % Gm::kMasks];
+      const bool none = t < none_hi || t >= none_lo;
+      // every row of the warp sees all of the tile or nothing
+      const bool plain = __all_sync(kFull, ok && mask == 0xF && t < t_full && (none || (t >= whole_lo && t < whole_hi)));
+      tc::fence_after_sync();
+      float cj[4], vr[4];  // a row that sees nothing of a plain tile gets arguments of 0 x - inf
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        cj[j] = none ? 0.f : sl2;
+        vr[j] = 1.f;
+      }
+      float top = vref;  // FP8: the largest V scale so far, this tile's included (the same on every thread)
+      if constexpr (Gm::kFp8) {
+        const float4 k4 = *reinterpret_cast<const float4*>(tile_sk + (t & 3) * 4);
+        const float4 v4 = *reinterpret_cast<const float4*>(tile_sv + (t & 3) * 4);
+        const float k[4] = {k4.x, k4.y, k4.z, k4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          cj[j] *= k[j];
+          vr[j] = v[j];
+          top = fmaxf(top, v[j]);  // a block without data has scale 0
+        }
+        if (top > vref) rvref = 1.f / top;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) vr[j] *= rvref;  // <= 1 up to an ulp
+      }
+      uint32_t pk[32];
+      float sum = 0.f;
+      // the usual way, against the max as this warp knows it
+      auto usual = [&]() -> bool {
+        if (!__all_sync(kFull, plain && top == vref && (none || m != -INFINITY))) return false;
+        sum = exponents<false, Gm::kFp8, kBfMma>(t_s, none ? -INFINITY : -m, cj, vr, 0, pk);
+        return __all_sync(kFull, sum <= kMost);
+      };
+      bool done = usual();
+      if constexpr (H == 2) {
+        // this warp's turn: the tile before has been handed over
+        if (u > 0)
+          ok = (mbar_test_wait(my_turn, (uint32_t)(u - 1) & 1u) ||
+                mbar_wait_bounded(my_turn, (uint32_t)(u - 1) & 1u, p.timeout_ns)) && ok;
+        if (row_moves[wg * 4 + quad] != moves) {
+          moves = row_moves[wg * 4 + quad];
+          follow();
+          done = usual();
+        }
+      }
+      if (!__all_sync(kFull, done && ok)) {
+        // ---- the general way: masks, max, rescaling ----
+        if (!__all_sync(kFull, ok)) {
+          aborted = true;
+          break;
+        }
+        const int base = (t0 + t) * kN;
+        if constexpr (Gm::k16) {
+          // V rows without valid data (past the states, or a block not loaded)
+          // are zeroed: P is 0 there, and 0 x NaN would poison O. Each row tile's
+          // warps zero them (the same zeros) before their P is handed over.
+          if (mask != 0xF || t >= t_full) {
+            ok = mbar_wait_bounded(&bar_vfull[stage_of(t)], lap_of(t), p.timeout_ns) && ok;
+            uint8_t* v_op = stage_at(stage_of(t)) + Gm::kOpBytes;
+            const int step = 32 * warps_of(wg);
+            for (int i = r; i < kN * Gm::NB * 8; i += step) {
+              const int rr = i / (Gm::NB * 8), k = i % (Gm::NB * 8);
+              if (((mask >> (rr >> 4)) & 1) && base + rr < L) continue;
+              *reinterpret_cast<uint4*>(v_op + (k >> 3) * kN * 128 + rr * 128 + ((k & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_smem_to_async();
+          }
+        }
+        // columns that the row sees, in blocks that hold data
+        uint64_t cols = 0;
+        {
+          const int a = min(max(my_lo - base, 0), kN), z = min(max(my_hi - base, 0), kN);
+          if (row_ok && a < z) cols = (z - a == 64 ? ~0ull : ((1ull << (z - a)) - 1)) << a;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((mask >> j) & 1)) cols &= ~(0xFFFFull << (16 * j));
+        }
+        const float mx = plain ? largest<false>(t_s, cj, 0) : largest<true>(t_s, cj, cols);
+        float fo = 1.f;  // rescale of l and O for a larger row max
+        if (mx > m + kLazy && !none) {
+          fo = ex2(m - mx);  // 0 when m was -inf
+          m = mx;
+        }
+        l *= fo;
+        if (Gm::kFp8 && top > vref) {  // O moves to units of a larger V scale
+          fo *= vref / top;
+          vref = top;
+        }
+        if (plain)
+          sum = exponents<false, Gm::kFp8, kBfMma>(t_s, none ? -INFINITY : -m, cj, vr, 0, pk);
+        else
+          sum = exponents<true, Gm::kFp8, kBfMma>(t_s, m == -INFINITY ? 0.f : -m, cj, vr, cols, pk);
+        // O is rescaled once PV(u - 1) is done, before PV(u) is issued (which waits for P(u))
+        if (u > 0 && __any_sync(kFull, fo != 1.f)) {
+          ok = mbar_wait_bounded(&my_pv[(u - 1) & 1], (uint32_t)((u - 1) >> 1) & 1u, p.timeout_ns) && ok;
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tc::tmem_ld32(t_row + c0, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fo);
+            tc::tmem_st32(t_row + c0, o);
+          }
+        }
+        if constexpr (H == 2) {
+          row_max[wg * kM + r] = m;
+          ++moves;
+          if (lane == 0) row_moves[wg * 4 + quad] = moves;
+        }
+      }
+      l += sum;
+      // P over this row's columns of S, then the warp's share is handed over
+      tc::tmem_st32(t_s, pk);
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&my_p[u & 1]);
+        if constexpr (H == 2) mbar_arrive(my_turn);
+      }
+    }
+
+    if (!aborted && U > 0) {
+      ok = mbar_wait_bounded(&my_pv[(U - 1) & 1], (uint32_t)((U - 1) >> 1) & 1u, p.timeout_ns) && ok;
+      aborted = !__all_sync(kFull, ok);
+    }
+    if (aborted && lane == 0) {
+      *abort_flag = 1;
+      raise_flag(p.err, PQKV_DEVERR_TIMEOUT);
+    }
+    // every tile of the half is handed over: the max is final
+    if constexpr (H == 2) {
+      if (!aborted && U > 0 && row_moves[wg * 4 + quad] != moves) follow();
+      row_sum[(group * 2 + wg) * kM + r] = l;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (*abort_flag) {  // copies in flight land before the CTA goes on
+    if (tid == 0) {
+      bool drained = true;
+      for (int kv = 0; kv < Gm::kProducers; ++kv)
+        for (int t = max(0, n_issued[kv] - ns); t < n_issued[kv]; ++t)
+          drained = mbar_wait_bounded(kv ? &bar_vfull[stage_of(t)] : &bar_full[stage_of(t)], lap_of(t), p.drain_ns) &&
+                    drained;
+      if (!drained) raise_flag(p.err, PQKV_DEVERR_DRAIN);
+    }
+    __syncthreads();
+  }
+  tc::fence_after_sync();
+  // the groups of a row share out its channels
+  const uint32_t t_row = tmem + 256u * wg + ((uint32_t)(32 * quad) << 16);
+  const bool holds_row = is_compute && quad < warps_of(wg) && (dup || !one_tile || wg == 0);
+  if (H == 2 && holds_row) l = row_sum[wg * kM + r] + row_sum[(2 + wg) * kM + r];
+  if (!dup && p.splits == 1) {
+    if (holds_row && !*abort_flag) {
+      const float inv = l > 0.f ? (Gm::kFp8 ? vref : 1.f) / l : 0.f;
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + orow;
+#pragma unroll 1
+      for (int c0 = group * (D / H); c0 < (group + 1) * (D / H); c0 += 32) {
+        uint32_t o[32];
+        tc::tmem_ld32(t_row + c0, o);
+        if (row_ok) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_f32x2(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv,
+                                QBF16);
+            *reinterpret_cast<uint4*>(dst + c0 + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc::fence_before_sync();
+    }
+    __syncthreads();  // tensor memory is read
+  } else {
+    // Parts of the same rows: the halves of a CTA (dup) and the CTAs of the
+    // cluster. Each leaves its O, m and l in shared memory (the stages and
+    // operands are done with), then the CTAs share out the rows, a group of
+    // lanes joining a row from all parts. Chunk c of a row lies at c ^ row, so
+    // that 32 rows' equal chunks fall in different banks.
+    constexpr int kChunks = D / 4;  // 16-byte pieces of a row of O
+    float2* s_stat = reinterpret_cast<float2*>(smem + 2 * kM * D * 4);
+    if (holds_row) {
+      const int slot = wg * kM + r;
+      if (group == 0) s_stat[slot] = make_float2(m, l);
+      if (tiles_of(wg) > 0) {
+        const float vs = Gm::kFp8 ? vref : 1.f;
+#pragma unroll 1
+        for (int c0 = group * (D / H); c0 < (group + 1) * (D / H); c0 += 32) {
+          uint32_t o[32];
+          tc::tmem_ld32(t_row + c0, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int c = (c0 / 4 + k) ^ (slot & (kChunks - 1));
+            *reinterpret_cast<float4*>(smem + ((size_t)slot * kChunks + c) * 16) =
+                make_float4(__uint_as_float(o[4 * k]) * vs, __uint_as_float(o[4 * k + 1]) * vs,
+                            __uint_as_float(o[4 * k + 2]) * vs, __uint_as_float(o[4 * k + 3]) * vs);
+          }
+        }
+      }
+      tc::fence_before_sync();
+    }
+    if (p.splits > 1) cluster_sync();
+    else __syncthreads();
+    const uint32_t part_at = smem_u32(smem), stat_at = smem_u32(s_stat);
+    constexpr int kRowsPerWarp = 32 / kChunks;  // 32 (D = 128) or 16 lanes a row
+    constexpr int kWarps = Gm::kThreads / 32;
+    const int c = lane % kChunks;
+    for (int i = (rank * kWarps + warp) * kRowsPerWarp + lane / kChunks; i < n_rows;
+         i += p.splits * kWarps * kRowsPerWarp) {
+      // part k = s par + e: half e of CTA s; 8 parts at once, loads past the last
+      // one repeat it and count nothing
+      const int parts = p.splits * par;
+      auto at_of = [&](int k) { return i + (k & (par - 1)) * kM; };
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float mx = -INFINITY, sum = 0.f;
+#pragma unroll 1
+      for (int k0 = 0; k0 < parts; k0 += 8) {
+        float2 st[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int k = min(k0 + e, parts - 1);
+          st[e] = ld_peer2(stat_at + (uint32_t)at_of(k) * 8, k >> pshift);
+        }
+        float top = mx;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (k0 + e >= parts) st[e].x = -INFINITY;
+          top = fmaxf(top, st[e].x);
+        }
+        const float f = mx == top ? 1.f : ex2(mx - top);
+        mx = top;
+        sum *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+        for (int e0 = 0; e0 < 8; e0 += 4) {
+          float4 o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = min(k0 + e0 + e, parts - 1), at = at_of(k);
+            o[e] = ld_peer4(part_at + (uint32_t)(at * kChunks + (c ^ (at & (kChunks - 1)))) * 16, k >> pshift);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = st[e0 + e];
+            if (a.x == -INFINITY) continue;  // a part without tiles leaves no O
+            const float w = ex2(a.x - mx);
+            sum = fmaf(w, a.y, sum);
+            acc = make_float4(fmaf(w, o[e].x, acc.x), fmaf(w, o[e].y, acc.y), fmaf(w, o[e].z, acc.z),
+                              fmaf(w, o[e].w, acc.w));
+          }
+        }
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      uint16_t* dst = static_cast<uint16_t*>(p.out) +
+                      ((size_t)(q0 + mt0 * TOK + i / G) * p.Hq + (size_t)h * G + i % G) * D + 4 * c;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_f32x2(acc.x * inv, acc.y * inv, QBF16), pack_f32x2(acc.z * inv, acc.w * inv, QBF16));
+    }
+    if (p.splits > 1) cluster_sync();  // no CTA leaves while another reads its parts
+  }
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// CTAs per row-tile pair: doubled while the doubled grid still fits the GPU at
+// one CTA per SM and every CTA keeps a tile.
 int cross_splits(long long ctas, int maxblk, int sms) {
   const int tiles = (maxblk * kBlock + kN - 1) / kN;
   int s = 1;
@@ -28,25 +924,24 @@ int cross_splits(long long ctas, int maxblk, int sms) {
 }
 
 template <int KVF, int D, bool QBF16>
-cudaError_t launch_cross_t(const CUtensorMap& tmap, PrefillParams p, int sms, cudaStream_t st) {
-  auto kern = paged_prefill_kernel<KVF, D, QBF16, true>;
-  constexpr int smem = PrefillGeom<KVF, D>::kSmem;
-  constexpr int NWG = PrefillGeom<KVF, D>::NWG;
+cudaError_t launch_cross_t(const CUtensorMap& tmap, CrossParams p, int sms, cudaStream_t st) {
+  using Gm = CrossGeom<KVF, D>;
+  auto kern = paged_cross_kernel<KVF, D, QBF16>;
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(configured.load() & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  const unsigned pairs = (unsigned)(p.B * ((p.tiles_per_seq + NWG - 1) / NWG));
+  const unsigned pairs = (unsigned)(p.B * ((p.tiles_per_seq + 1) / 2));
   p.splits = cross_splits((long long)pairs * p.Hkv, p.maxblk, sms);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pairs, (unsigned)p.Hkv, (unsigned)p.splits);
-  cfg.blockDim = dim3(PrefillGeom<KVF, D>::kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.blockDim = dim3(Gm::kThreads);
+  cfg.dynamicSmemBytes = Gm::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -63,7 +958,19 @@ cudaError_t launch_cross_t(const CUtensorMap& tmap, PrefillParams p, int sms, cu
 
 }  // namespace
 
-cudaError_t launch_cross(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap16, const PrefillParams& p, int sms,
+size_t cross_smem_bytes(int kv_dtype, int D) {
+#define PQKV_CS(F) \
+  if (kv_dtype == F) return D == 128 ? CrossGeom<F, 128>::kSmem : CrossGeom<F, 64>::kSmem;
+  PQKV_CS(PQKV_DTYPE_FP16)
+  PQKV_CS(PQKV_DTYPE_BF16)
+  PQKV_CS(PQKV_DTYPE_FP8_E4M3)
+  PQKV_CS(PQKV_DTYPE_FP8_E5M2)
+  PQKV_CS(PQKV_DTYPE_FP4_E2M1)
+#undef PQKV_CS
+  return 0;
+}
+
+cudaError_t launch_cross(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap16, const CrossParams& p, int sms,
                          cudaStream_t st) {
 #define PQKV_CR(KVF, DD, QB) \
   if (kv_dtype == KVF && D == DD && q_bf16 == QB) return launch_cross_t<KVF, DD, QB>(tmap16, p, sms, st);

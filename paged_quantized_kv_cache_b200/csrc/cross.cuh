@@ -1,0 +1,43 @@
+// cross.cuh -- attention of decoder tokens to an encoder's cached states.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+
+namespace pqkv {
+
+// Query rows (tokens x query heads) per KV head up to which the few-rows kernel runs.
+constexpr int kFewColumns = 16;
+
+struct CrossParams {
+  const void* q;                // [cu_q[B]][Hq][D]
+  void* out;                    // same shape and type as q
+  const uint8_t* cache;
+  const uint8_t* scales;
+  const uint8_t* oidx;
+  const uint8_t* oval;
+  const int32_t* cu_q;          // [B + 1] query-token offsets
+  const int32_t* kv_lens;       // [B] states of each sequence
+  const int32_t* block_tables;  // [B][maxblk]
+  const int32_t* ranges;        // [cu_q[B]][2] positions each query token sees, or null: all
+  int32_t* err;
+  int B, Hq, Hkv, G, nb, maxblk;
+  int max_q;                    // query tokens of the longest sequence
+  int tiles_per_seq;            // 128-row query tiles per sequence
+  int splits;                   // CTAs of a cluster, which share the states of their rows (set by the launcher)
+  float scale_log2;             // softmax scale * log2(e)
+  uint64_t timeout_ns;          // limit of a wait before a warp gives up
+  uint64_t drain_ns;            // after giving up: limit of the wait for work still in flight
+};
+
+// Tiles of 128 query rows on tcgen05 (cross.cu; the prefill's tensor map for
+// 16-bit caches), or at most kFewColumns rows per KV head (cross_few.cu; the
+// decode's tensor map).
+cudaError_t launch_cross(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap16, const CrossParams& p, int sms,
+                         cudaStream_t st);
+cudaError_t launch_cross_few(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap, const CrossParams& p, int sms,
+                             cudaStream_t st);
+size_t cross_smem_bytes(int kv_dtype, int D);
+
+}  // namespace pqkv

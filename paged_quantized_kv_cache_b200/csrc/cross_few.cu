@@ -18,8 +18,9 @@
 #include <atomic>
 #include <climits>
 
+#include "cluster.cuh"
+#include "cross.cuh"
 #include "decode_block.cuh"
-#include "prefill.cuh"
 
 namespace pqkv {
 
@@ -47,31 +48,9 @@ struct FewGeom {
   static_assert(2 * (kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ float ld_peer(uint32_t addr, int rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(peer_addr(addr, rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_peer4(uint32_t addr, int rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(peer_addr(addr, rank))
-               : "memory");
-  return v;
-}
-
 template <int KVF, int D, bool QBF16, int NT>
 __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
-    cross_few_kernel(const __grid_constant__ CUtensorMap tmap, const PrefillParams p) {
+    cross_few_kernel(const __grid_constant__ CUtensorMap tmap, const CrossParams p) {
   using Gm = DecodeGeom<KVF, D, NT>;
   using Fg = FewGeom<KVF, D, NT>;
   constexpr int NC = Fg::NC, NW = Fg::kWarps, NS = Fg::kStages, KT = D / 16;
@@ -90,7 +69,7 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
   const int b = pair / p.Hkv, h = pair - b * p.Hkv;
 
   const int q0 = p.cu_q[b], qn = p.cu_q[b + 1] - q0;
-  const int L = p.seq_lens[b];
+  const int L = p.kv_lens[b];
   const bool rejected = L < 0 || L > kBlock * p.maxblk;
   if (h == 0 && rank == 0 && tid == 0 && (qn > p.max_q || (qn > 0 && rejected))) raise_flag(p.err, PQKV_DEVERR_SEQ_LEN);
   const int nc = min(qn, p.max_q) * G;  // columns: token n / G, query head n % G
@@ -511,7 +490,7 @@ int few_splits(long long pairs, int maxblk, int warps, int sms) {
 }
 
 template <int KVF, int D, bool QBF16, int NT>
-cudaError_t launch_few_t(const CUtensorMap& tmap, PrefillParams p, int sms, cudaStream_t st) {
+cudaError_t launch_few_t(const CUtensorMap& tmap, CrossParams p, int sms, cudaStream_t st) {
   using Fg = FewGeom<KVF, D, NT>;
   auto kern = cross_few_kernel<KVF, D, QBF16, NT>;
   static std::atomic<uint64_t> configured{0};
@@ -546,7 +525,7 @@ cudaError_t launch_few_t(const CUtensorMap& tmap, PrefillParams p, int sms, cuda
 
 }  // namespace
 
-cudaError_t launch_cross_few(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap, const PrefillParams& p,
+cudaError_t launch_cross_few(int kv_dtype, int D, bool q_bf16, const CUtensorMap& tmap, const CrossParams& p,
                              int sms, cudaStream_t st) {
 #define PQKV_FEW(KVF, DD, QB)                                                             \
   if (kv_dtype == KVF && D == DD && q_bf16 == QB)                                         \
