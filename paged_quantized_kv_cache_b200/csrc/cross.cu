@@ -99,7 +99,7 @@ struct CrossGeom {
   static constexpr int oKop = oStage + kStages * kStageBytes;
   static constexpr int oVop = oKop + kKops * kOpBytes;
   static constexpr int oMisc = oVop + kVops * kOpBytes;
-  static constexpr int kBars = 4 * kMaxStages + 12 + 4 + 2 + 3 + 8 + 2;
+  static constexpr int kBars = 4 * kMaxStages + 12 + 4 + 2 + 3 + 8 + 2 + 1;
   static constexpr int oScales = oMisc + (kBars * 8 + 15) / 16 * 16;  // FP8 scales of tile t % 4: K [4][4], V [4][4]
   static constexpr int oWords = oScales + 128;
   static constexpr int kWords = kMasks + kMaxStages + 1 + 2 + 8 + 2 + 1;
@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   uint64_t* bar_vfree = bar_kfree + 2;           // [3] quantized: every PV(t) done (vop[t % 3])
   uint64_t* bar_turn = bar_vfree + 3;            // [2][4] H = 2: tile u of these 32 rows handed over (phase u)
   uint64_t* bar_drain = bar_turn + 8;            // [2] every product an MMA warp issued has completed
+  uint64_t* bar_q = bar_drain + 2;               // the Q tiles are there (one arrival per compute warp)
   float* tile_sk = reinterpret_cast<float*>(smem + Gm::oScales);  // [4][4] FP8 K scales of tile t % 4
   float* tile_sv = tile_sk + 16;                                  // [4][4] FP8 V scales
   volatile int* tile_mask = reinterpret_cast<volatile int*>(smem + Gm::oWords);  // [kMasks] blocks of tile t that hold data
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   auto stage_of = [&](int t) { return ns == 4 ? t & 3 : t % 5; };
   auto lap_of = [&](int t) { return (uint32_t)(ns == 4 ? t >> 2 : t / 5) & 1u; };
 
-  // ---- setup: tensor memory, barriers, Q tiles ----
+  // ---- setup: tensor memory, barriers ----
   if (warp == 0) tc::tmem_alloc(tmem_slot, 512);
   if (tid == 32 * Gm::kProducer) {
     if constexpr (Gm::k16) prefetch_tensormap(&tmap);
@@ -312,54 +313,11 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     for (int i = 0; i < 2; ++i) mbar_init(&bar_kfree[i], consumers);
     for (int i = 0; i < 3; ++i) mbar_init(&bar_vfree[i], consumers);
     for (int i = 0; i < 2; ++i) mbar_init(&bar_drain[i], 1);
+    mbar_init(bar_q, Gm::kComputeWarps);
     *abort_flag = 0;
     n_issued[0] = n_issued[1] = 0;
     fence_mbar_init();
   }
-  // softmax scale in log2 units of this thread's row, times 2^e when the row's
-  // bf16 query was scaled by 2^-e before narrowing to f16 (quantized caches)
-  float sl2 = p.scale_log2;
-  if (is_compute) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow);
-    float qmul = 1.f;
-    if constexpr (!Gm::k16 && QBF16) {
-      // the power of two 2^-e that brings the row's largest |q| into
-      // [2^13, 2^14): exact, and far from both ends of the f16 range
-      float mx = 0.f;
-      if (row_ok) {
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = __ldg(src + c);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-        }
-      }
-      const int ex = (mx > 0.f && mx <= FLT_MAX) ? ilogbf(mx) - 13 : 0;
-      qmul = ldexpf(1.f, -ex);
-      sl2 = p.scale_log2 * ldexpf(1.f, ex);
-    }
-    if (!one_tile || wg == 0) {
-      // this thread's share of its row of the Q tile, converted to the operand
-      // type, 16-byte chunks swizzled; rows past the end are zeros
-      uint8_t* sQ = smem + Gm::oQ + (one_tile ? 0 : wg) * Gm::kQBytes;
-#pragma unroll 4
-      for (int c = group * (D / 8 / H); c < (group + 1) * (D / 8 / H); ++c) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row_ok) v = __ldg(src + c);
-        if constexpr (!Gm::k16 && QBF16) {
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = to_f16x2(__uint_as_float(w[i] << 16) * qmul, __uint_as_float(w[i] & 0xFFFF0000u) * qmul);
-          v = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        *reinterpret_cast<uint4*>(sQ + (c >> 3) * (kM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-      }
-    }
-  }
-  tc::fence_smem_to_async();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -470,6 +428,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
         tc::commit(Gm::k16 ? &bar_vempty[stage_of(t)] : &bar_vfree[t % 3]);  // V may be refilled
       }
     };
+    wait(bar_q, 0);
     for (int u = 0; u < min(2, U) && good; ++u) {
       wait_k(w0 + (u << pshift));
       if (good) issue_s(u);
@@ -606,14 +565,59 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
         raise_flag(p.err, PQKV_DEVERR_TIMEOUT);
       }
     }
-  } else if (quad < warps_of(wg)) {
+  } else {
     // ================= compute warps: row r of half wg, its tiles u = group, group + H, ... =================
+    // softmax scale in log2 units of this thread's row, times 2^e when the row's
+    // bf16 query was scaled by 2^-e before narrowing to f16 (quantized caches)
+    float sl2 = p.scale_log2;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow);
+    float qmul = 1.f;
+    if constexpr (!Gm::k16 && QBF16) {
+      // the power of two 2^-e that brings the row's largest |q| into
+      // [2^13, 2^14): exact, and far from both ends of the f16 range
+      float mx = 0.f;
+      if (row_ok) {
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = __ldg(src + c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+        }
+      }
+      const int ex = (mx > 0.f && mx <= FLT_MAX) ? ilogbf(mx) - 13 : 0;
+      qmul = ldexpf(1.f, -ex);
+      sl2 = p.scale_log2 * ldexpf(1.f, ex);
+    }
+    if (!one_tile || wg == 0) {
+      // this thread's share of its row of the Q tile, converted to the operand
+      // type, 16-byte chunks swizzled; rows past the end are zeros
+      uint8_t* sQ = smem + Gm::oQ + (one_tile ? 0 : wg) * Gm::kQBytes;
+#pragma unroll 4
+      for (int c = group * (D / 8 / H); c < (group + 1) * (D / 8 / H); ++c) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row_ok) v = __ldg(src + c);
+        if constexpr (!Gm::k16 && QBF16) {
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = to_f16x2(__uint_as_float(w[i] << 16) * qmul, __uint_as_float(w[i] & 0xFFFF0000u) * qmul);
+          v = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *reinterpret_cast<uint4*>(sQ + (c >> 3) * (kM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+      }
+    }
+    tc::fence_smem_to_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_q);
     const uint32_t t_row = tmem + 256u * wg + ((uint32_t)(32 * quad) << 16);
     uint64_t* my_s = bar_s + 2 * wg;
     uint64_t* my_p = bar_p + 2 * wg;
     uint64_t* my_pv = bar_pv + 2 * wg;
     uint64_t* my_turn = bar_turn + 4 * wg + quad;
-    const int w0 = dup ? wg : 0, U = tiles_of(wg);
+    // a warp without rows has only zeros to leave in the Q tile
+    const int w0 = dup ? wg : 0, U = quad < warps_of(wg) ? tiles_of(wg) : 0;
     bool ok = true;      // no wait of this thread has timed out
     float rvref = 0.f;   // FP8: 1 / vref (0 while vref is 0)
     int moves = 0;       // H = 2: moves of the max that this warp has followed
@@ -798,115 +802,113 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   const uint32_t t_row = tmem + 256u * wg + ((uint32_t)(32 * quad) << 16);
   const bool holds_row = is_compute && quad < warps_of(wg) && (dup || !one_tile || wg == 0);
   if (H == 2 && holds_row) l = row_sum[wg * kM + r] + row_sum[(2 + wg) * kM + r];
-  if (!dup && p.splits == 1) {
-    if (holds_row && !*abort_flag) {
-      const float inv = l > 0.f ? (Gm::kFp8 ? vref : 1.f) / l : 0.f;
+  // Partial results in shared memory (the stages and operands are done with):
+  // chunk c (16 bytes) of row `slot` lies at c ^ slot, so that 32 rows' equal
+  // chunks fall in different banks.
+  constexpr int kChunks = D / 4;  // 16-byte pieces of a row of O
+  float2* s_stat = reinterpret_cast<float2*>(smem + 2 * kM * D * 4);
+  auto chunk_at = [&](int slot, int c) { return (uint32_t)(slot * kChunks + (c ^ (slot & (kChunks - 1)))) * 16; };
+  auto leave_part = [&]() {  // this thread's channels of its row, and m and l
+    const int slot = wg * kM + r;
+    if (group == 0) s_stat[slot] = make_float2(m, l);
+    if (tiles_of(wg) > 0) {
+      const float vs = Gm::kFp8 ? vref : 1.f;
+#pragma unroll 1
+      for (int c0 = group * (D / H); c0 < (group + 1) * (D / H); c0 += 32) {
+        uint32_t o[32];
+        tc::tmem_ld32(t_row + c0, o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<float4*>(smem + chunk_at(slot, c0 / 4 + k)) =
+              make_float4(__uint_as_float(o[4 * k]) * vs, __uint_as_float(o[4 * k + 1]) * vs,
+                          __uint_as_float(o[4 * k + 2]) * vs, __uint_as_float(o[4 * k + 3]) * vs);
+      }
+    }
+    tc::fence_before_sync();
+  };
+  if (p.splits == 1) {
+    // the second half of a CTA that shares a row tile (dup) leaves its part to the first
+    if (dup && wg == 1 && holds_row) leave_part();
+    if (dup) __syncthreads();
+    if (holds_row && (!dup || wg == 0) && !*abort_flag) {
+      float2 st = make_float2(-INFINITY, 0.f);
+      if (dup) st = s_stat[kM + r];
+      const float mx = fmaxf(m, st.x);
+      const float f = m == -INFINITY ? 0.f : ex2(m - mx), f2 = st.x == -INFINITY ? 0.f : ex2(st.x - mx);
+      const float sum = f * l + f2 * st.y, inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float a = f * inv * (Gm::kFp8 ? vref : 1.f), a2 = f2 * inv;
       uint16_t* dst = static_cast<uint16_t*>(p.out) + orow;
 #pragma unroll 1
       for (int c0 = group * (D / H); c0 < (group + 1) * (D / H); c0 += 32) {
         uint32_t o[32];
         tc::tmem_ld32(t_row + c0, o);
-        if (row_ok) {
+        if (!row_ok) continue;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
+        for (int k = 0; k < 4; ++k) {
+          float v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_f32x2(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv,
-                                QBF16);
-            *reinterpret_cast<uint4*>(dst + c0 + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[8 * k + i]) * a;
+          if (a2 > 0.f) {  // a half without tiles leaves no O
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float4 w = *reinterpret_cast<const float4*>(smem + chunk_at(kM + r, c0 / 4 + 2 * k + i));
+              v[4 * i] = fmaf(w.x, a2, v[4 * i]);
+              v[4 * i + 1] = fmaf(w.y, a2, v[4 * i + 1]);
+              v[4 * i + 2] = fmaf(w.z, a2, v[4 * i + 2]);
+              v[4 * i + 3] = fmaf(w.w, a2, v[4 * i + 3]);
+            }
           }
+          *reinterpret_cast<uint4*>(dst + c0 + 8 * k) =
+              make_uint4(pack_f32x2(v[0], v[1], QBF16), pack_f32x2(v[2], v[3], QBF16), pack_f32x2(v[4], v[5], QBF16),
+                         pack_f32x2(v[6], v[7], QBF16));
         }
       }
       tc::fence_before_sync();
     }
     __syncthreads();  // tensor memory is read
   } else {
-    // Parts of the same rows: the halves of a CTA (dup) and the CTAs of the
-    // cluster. Each leaves its O, m and l in shared memory (the stages and
-    // operands are done with), then the CTAs share out the rows, a group of
-    // lanes joining a row from all parts. Chunk c of a row lies at c ^ row, so
-    // that 32 rows' equal chunks fall in different banks.
-    constexpr int kChunks = D / 4;  // 16-byte pieces of a row of O
-    float2* s_stat = reinterpret_cast<float2*>(smem + 2 * kM * D * 4);
-    if (holds_row) {
-      const int slot = wg * kM + r;
-      if (group == 0) s_stat[slot] = make_float2(m, l);
-      if (tiles_of(wg) > 0) {
-        const float vs = Gm::kFp8 ? vref : 1.f;
-#pragma unroll 1
-        for (int c0 = group * (D / H); c0 < (group + 1) * (D / H); c0 += 32) {
-          uint32_t o[32];
-          tc::tmem_ld32(t_row + c0, o);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int c = (c0 / 4 + k) ^ (slot & (kChunks - 1));
-            *reinterpret_cast<float4*>(smem + ((size_t)slot * kChunks + c) * 16) =
-                make_float4(__uint_as_float(o[4 * k]) * vs, __uint_as_float(o[4 * k + 1]) * vs,
-                            __uint_as_float(o[4 * k + 2]) * vs, __uint_as_float(o[4 * k + 3]) * vs);
-          }
-        }
-      }
-      tc::fence_before_sync();
-    }
-    if (p.splits > 1) cluster_sync();
-    else __syncthreads();
+    // Parts of the same rows: the CTAs of the cluster, and the halves of each
+    // (dup). Each leaves its O, m and l in shared memory, then the CTAs share out
+    // the rows, a group of lanes joining a row from all parts.
+    if (holds_row) leave_part();
+    cluster_sync();
     const uint32_t part_at = smem_u32(smem), stat_at = smem_u32(s_stat);
     constexpr int kRowsPerWarp = 32 / kChunks;  // 32 (D = 128) or 16 lanes a row
     constexpr int kWarps = Gm::kThreads / 32;
     const int c = lane % kChunks;
-    for (int i = (rank * kWarps + warp) * kRowsPerWarp + lane / kChunks; i < n_rows;
-         i += p.splits * kWarps * kRowsPerWarp) {
-      // part k = s par + e: half e of CTA s; 8 parts at once, loads past the last
-      // one repeat it and count nothing
-      const int parts = p.splits * par;
-      auto at_of = [&](int k) { return i + (k & (par - 1)) * kM; };
+    // a group of kChunks lanes per row: lane k holds the statistics of part k =
+    // s par + e (half e of CTA s), then every lane adds up its chunk of all parts
+    const int parts = p.splits << pshift;  // at most 16
+    for (int i0 = (rank * kWarps + warp) * kRowsPerWarp; i0 < n_rows; i0 += p.splits * kWarps * kRowsPerWarp) {
+      const int i = min(i0 + lane / kChunks, n_rows - 1);
+      float2 st = make_float2(-INFINITY, 0.f);
+      if (c < parts) st = ld_peer2(stat_at + (uint32_t)(i + (c & (par - 1)) * kM) * 8, c >> pshift);
+      float mx = st.x;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o, 16));
+      // a part without tiles leaves no O and counts nothing
+      float w = st.x == -INFINITY ? 0.f : ex2(st.x - mx);
+      float sum = w * st.y;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o, 16);
+      sum = __shfl_sync(kFull, sum, 0, kChunks);
+      w = w > 0.f && sum > 0.f ? w / sum : 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float mx = -INFINITY, sum = 0.f;
-#pragma unroll 1
-      for (int k0 = 0; k0 < parts; k0 += 8) {
-        float2 st[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = min(k0 + e, parts - 1);
-          st[e] = ld_peer2(stat_at + (uint32_t)at_of(k) * 8, k >> pshift);
-        }
-        float top = mx;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (k0 + e >= parts) st[e].x = -INFINITY;
-          top = fmaxf(top, st[e].x);
-        }
-        const float f = mx == top ? 1.f : ex2(mx - top);
-        mx = top;
-        sum *= f;
-        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-#pragma unroll
-        for (int e0 = 0; e0 < 8; e0 += 4) {
-          float4 o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = min(k0 + e0 + e, parts - 1), at = at_of(k);
-            o[e] = ld_peer4(part_at + (uint32_t)(at * kChunks + (c ^ (at & (kChunks - 1)))) * 16, k >> pshift);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 a = st[e0 + e];
-            if (a.x == -INFINITY) continue;  // a part without tiles leaves no O
-            const float w = ex2(a.x - mx);
-            sum = fmaf(w, a.y, sum);
-            acc = make_float4(fmaf(w, o[e].x, acc.x), fmaf(w, o[e].y, acc.y), fmaf(w, o[e].z, acc.z),
-                              fmaf(w, o[e].w, acc.w));
-          }
-        }
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k) {
+        const int at = i + (k & (par - 1)) * kM;
+        const float4 o = ld_peer4(part_at + chunk_at(at, c), k >> pshift);
+        const float f = __shfl_sync(kFull, w, k, kChunks);
+        if (f != 0.f)
+          acc = make_float4(fmaf(f, o.x, acc.x), fmaf(f, o.y, acc.y), fmaf(f, o.z, acc.z), fmaf(f, o.w, acc.w));
       }
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      if (i0 + lane / kChunks >= n_rows) continue;
       uint16_t* dst = static_cast<uint16_t*>(p.out) +
                       ((size_t)(q0 + mt0 * TOK + i / G) * p.Hq + (size_t)h * G + i % G) * D + 4 * c;
       *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack_f32x2(acc.x * inv, acc.y * inv, QBF16), pack_f32x2(acc.z * inv, acc.w * inv, QBF16));
+          make_uint2(pack_f32x2(acc.x, acc.y, QBF16), pack_f32x2(acc.z, acc.w, QBF16));
     }
-    if (p.splits > 1) cluster_sync();  // no CTA leaves while another reads its parts
+    cluster_sync();  // no CTA leaves while another reads its parts
   }
   if (warp == 0) {
     tc::fence_after_sync();
@@ -915,11 +917,11 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
 }
 
 // CTAs per row-tile pair: doubled while the doubled grid still fits the GPU at
-// one CTA per SM and every CTA keeps a tile.
+// one CTA per SM and every CTA keeps two tiles, one for each of its halves.
 int cross_splits(long long ctas, int maxblk, int sms) {
   const int tiles = (maxblk * kBlock + kN - 1) / kN;
   int s = 1;
-  while (2 * s <= kMaxSplits && ctas * 2 * s <= sms && 2 * s <= tiles) s *= 2;
+  while (2 * s <= kMaxSplits && ctas * 2 * s <= sms && 2 * s * 2 <= tiles) s *= 2;
   return s;
 }
 
