@@ -327,54 +327,68 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
 
   if (warp >= Gm::kProducer && warp < Gm::kMma) {
     // ================= producers: KV tiles (16-bit: K, and V) into the stage rings =================
-    if (lane == 0) {
-      const int kv = warp - Gm::kProducer;  // 16-bit: 0 = K, 1 = V
-      uint64_t* full = kv ? bar_vfull : bar_full;
-      uint64_t* empty = kv ? bar_vempty : bar_empty;
-      int t = 0;
-      for (; t < T; ++t) {
-        const int s = stage_of(t);
-        if (t >= ns && !mbar_wait_bounded(&empty[s], lap_of(t) ^ 1u, p.timeout_ns)) break;
-        if (*abort_flag) break;
-        uint8_t* st = stage_at(s);
-        int ids[4];
+    // A lane per copy of a tile (copy `what` of block j), its block ids read two
+    // tiles ahead: read and issued one after the other by one thread, a tile
+    // took 1450 cycles, twice what a decode step's tile takes to arrive.
+    constexpr int kCopies = Gm::k16 ? Gm::NB : (Gm::kFp8 ? 2 : 4);  // per block
+    const int kv = warp - Gm::kProducer;  // 16-bit: 0 = K, 1 = V
+    uint64_t* full = kv ? bar_vfull : bar_full;
+    uint64_t* empty = kv ? bar_vempty : bar_empty;
+    const int j = lane / kCopies, what = lane % kCopies;
+    const int hi_blk = (hi + kBlock - 1) / kBlock;  // blocks from here on are not read
+    auto id_of = [&](int t) {
+      const int blk = 4 * (t0 + t) + j;
+      return j < 4 && t < T && blk < hi_blk ? __ldg(table + blk) : -1;
+    };
+    int id = id_of(0), id1 = id_of(1), id2 = id_of(2);
+    int t = 0, s = 0;
+    uint32_t lap = 0;
+    for (; t < T; ++t) {
+      if (t >= ns && !__all_sync(kFull, mbar_test_wait(&empty[s], lap ^ 1u) ||
+                                            mbar_wait_bounded(&empty[s], lap ^ 1u, p.timeout_ns)))
+        break;
+      if (*abort_flag) break;
+      const bool inside = j < 4 && 4 * (t0 + t) + j < hi_blk, good = inside && id >= 0 && id < p.nb;
+      if (inside && !good && what == 0) raise_flag(p.err, PQKV_DEVERR_BLOCK_ID);
+      const uint32_t votes = __ballot_sync(kFull, good && what == 0);
+      if (lane == 0) {
         int mask = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int blk = 4 * (t0 + t) + j;
-          ids[j] = blk * kBlock < hi ? __ldg(table + blk) : -1;
-          if (ids[j] >= 0 && ids[j] < p.nb) mask |= 1 << j;
-          else if (blk * kBlock < hi) raise_flag(p.err, PQKV_DEVERR_BLOCK_ID);
-        }
+        for (int i = 0; i < 4; ++i) mask |= ((votes >> (i * kCopies)) & 1) << i;
         // published to the consumers by the stage's barrier
         if (!Gm::k16) stage_mask[s] = mask;
         else if (kv == 0) tile_mask[t % Gm::kMasks] = mask;
         constexpr uint32_t kBytes = Gm::k16 ? (uint32_t)Gm::NB * kBlock * 128u : (uint32_t)(Gm::kRawTile + Gm::kSide);
         mbar_arrive_expect_tx(&full[s], (uint32_t)__popc(mask) * kBytes);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (!((mask >> j) & 1)) continue;
-          const size_t pair = (size_t)ids[j] * p.Hkv + h;
-          if constexpr (Gm::k16) {
-#pragma unroll
-            for (int bx = 0; bx < Gm::NB; ++bx)
-              tma_load_2d(st + kv * Gm::kOpBytes + bx * kN * 128 + j * kBlock * 128, &tmap, bx * 64,
-                          (int)pair * 32 + 16 * kv, &full[s]);
-          } else {
+      }
+      __syncwarp();
+      if (good) {
+        uint8_t* st = stage_at(s);
+        const size_t pair = (size_t)id * p.Hkv + h;
+        if constexpr (Gm::k16) {
+          tma_load_2d(st + kv * Gm::kOpBytes + what * kN * 128 + j * kBlock * 128, &tmap, what * 64,
+                      (int)pair * 32 + 16 * kv, &full[s]);
+        } else {
+          uint8_t* side = st + 4 * Gm::kRawTile + j * Gm::kSide;
+          if (what == 0)
             bulk_load(st + j * Gm::kRawTile, p.cache + pair * Gm::kRawTile, Gm::kRawTile, &full[s]);
-            uint8_t* side = st + 4 * Gm::kRawTile + j * Gm::kSide;
-            if constexpr (Gm::kFp8) {
-              bulk_load(side, p.scales + pair * 16, 16, &full[s]);
-            } else {
-              bulk_load(side, p.scales + pair * Gm::kScaleBytes, Gm::kScaleBytes, &full[s]);
-              bulk_load(side + Gm::kScaleBytes, p.oval + pair * Gm::kValBytes, Gm::kValBytes, &full[s]);
-              bulk_load(side + Gm::kScaleBytes + Gm::kValBytes, p.oidx + pair * 16, 16, &full[s]);
-            }
-          }
+          else if (what == 1)
+            bulk_load(side, p.scales + pair * Gm::kScaleBytes, Gm::kScaleBytes, &full[s]);
+          else if (what == 2)
+            bulk_load(side + Gm::kScaleBytes, p.oval + pair * Gm::kValBytes, Gm::kValBytes, &full[s]);
+          else
+            bulk_load(side + Gm::kScaleBytes + Gm::kValBytes, p.oidx + pair * 16, 16, &full[s]);
         }
       }
-      n_issued[kv] = t;
+      id = id1;
+      id1 = id2;
+      id2 = id_of(t + 3);
+      if (++s == ns) {
+        s = 0;
+        lap ^= 1u;
+      }
     }
+    if (lane == 0) n_issued[kv] = t;
   } else if (warp >= Gm::kMma && warp < Gm::kMma + 2) {
     // ================= MMA warp of half w: its products, KV tiles t = w0 + u par =================
     // Order: PV(u) once P(u) is in tensor memory, then S(u + 2) into the buffer
@@ -384,14 +398,31 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     // registers; one thread of it issues.
     const int w = warp - Gm::kMma, w0 = dup ? w : 0, U = tiles_of(w);
     bool good = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      good = __all_sync(kFull, mbar_test_wait(bar, parity) || mbar_wait_bounded(bar, parity, p.timeout_ns)) && good;
+    // both barriers' phases are complete
+    auto wait = [&](uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2) {
+      const bool a = mbar_test_wait(bar, parity), a2 = mbar_test_wait(bar2, parity2);
+      good = __all_sync(kFull, (a || mbar_wait_bounded(bar, parity, p.timeout_ns)) &&
+                                   (a2 || mbar_wait_bounded(bar2, parity2, p.timeout_ns))) &&
+             good;
     };
-    // K (with it, quantized, V) of tile t is there
-    auto wait_k = [&](int t) {
-      if constexpr (Gm::k16) wait(&bar_full[stage_of(t)], lap_of(t));
-      else wait(&bar_op[t & 3], (uint32_t)(t >> 2) & 1u);
+    // tiles in order: those whose S is issued next (k) and whose PV is (v), with
+    // their places in the rings
+    struct Place {
+      int t, s;
+      uint32_t lap;
     };
+    auto next = [&](Place& x) {
+      x.t += par;
+      x.s += par;
+      if (x.s >= ns) {
+        x.s -= ns;
+        x.lap ^= 1u;
+      }
+    };
+    Place k{w0, w0, 0}, v{w0, w0, 0};
+    // K (with it, quantized, V) of tile k.t is there
+    auto k_bar = [&]() { return Gm::k16 ? &bar_full[k.s] : &bar_op[k.t & 3]; };
+    auto k_parity = [&]() { return Gm::k16 ? k.lap : (uint32_t)(k.t >> 2) & 1u; };
     const uint32_t base = smem_u32(smem);
     const uint32_t qa = base + Gm::oQ + (one_tile ? 0 : w) * Gm::kQBytes;
     const bool issuer = tc::elect_one();
@@ -400,10 +431,9 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     };
     const uint64_t q_desc = tc::sw128_desc(qa, 16, 1024);
     auto issue_s = [&](int u) {
-      const int t = w0 + (u << pshift);
       tc::fence_after_sync();
       const uint32_t d = tmem + 256u * w + D + 64 * (u & 1);
-      const uint32_t ka = Gm::k16 ? stage_addr(stage_of(t)) : base + Gm::oKop + (t & 1) * Gm::kOpBytes;
+      const uint32_t ka = Gm::k16 ? stage_addr(k.s) : base + Gm::oKop + (k.t & 1) * Gm::kOpBytes;
       const uint64_t k_desc = tc::sw128_desc(ka, 16, 1024);
       if (issuer) {
 #pragma unroll
@@ -411,13 +441,13 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
           tc::mma_ss(d, q_desc + (kk >> 2) * (kM * 8) + (kk & 3) * 2, k_desc + (kk >> 2) * (kN * 8) + (kk & 3) * 2,
                      kIdescS, kk > 0);
         tc::commit(&bar_s[2 * w + (u & 1)]);
-        tc::commit(Gm::k16 ? &bar_empty[stage_of(t)] : &bar_kfree[t & 1]);  // K may be refilled
+        tc::commit(Gm::k16 ? &bar_empty[k.s] : &bar_kfree[k.t & 1]);  // K may be refilled
       }
+      next(k);
     };
     auto issue_pv = [&](int u) {
-      const int t = w0 + (u << pshift);
       tc::fence_after_sync();
-      const uint32_t va = Gm::k16 ? stage_addr(stage_of(t)) + Gm::kOpBytes : base + Gm::oVop + (t % 3) * Gm::kOpBytes;
+      const uint32_t va = Gm::k16 ? stage_addr(v.s) + Gm::kOpBytes : base + Gm::oVop + (v.t % 3) * Gm::kOpBytes;
       const uint64_t v_desc = tc::sw128_desc(va, kN * 128, 1024);
       const uint32_t o = tmem + 256u * w, pa = o + D + 64 * (u & 1);
       if (issuer) {
@@ -425,23 +455,22 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
         for (int kk = 0; kk < kN / 16; ++kk)
           tc::mma_ts(o, pa + kk * 8, v_desc + kk * 128, kIdescPV, u > 0 || kk > 0);
         tc::commit(&bar_pv[2 * w + (u & 1)]);
-        tc::commit(Gm::k16 ? &bar_vempty[stage_of(t)] : &bar_vfree[t % 3]);  // V may be refilled
+        tc::commit(Gm::k16 ? &bar_vempty[v.s] : &bar_vfree[v.t % 3]);  // V may be refilled
       }
+      next(v);
     };
-    wait(bar_q, 0);
     for (int u = 0; u < min(2, U) && good; ++u) {
-      wait_k(w0 + (u << pshift));
+      wait(k_bar(), k_parity(), bar_q, 0);
       if (good) issue_s(u);
     }
     for (int u = 0; u < U && good; ++u) {
-      const int t = w0 + (u << pshift);
-      wait(&bar_p[2 * w + (u & 1)], (uint32_t)(u >> 1) & 1u);
-      if constexpr (Gm::k16) wait(&bar_vfull[stage_of(t)], lap_of(t));
+      uint64_t* p_bar = &bar_p[2 * w + (u & 1)];
+      const uint32_t p_parity = (uint32_t)(u >> 1) & 1u;
+      wait(p_bar, p_parity, Gm::k16 ? &bar_vfull[v.s] : p_bar, Gm::k16 ? v.lap : p_parity);
       if (!good) break;
       issue_pv(u);
       if (u + 2 < U) {
-        wait_k(t + (2 << pshift));
-        wait(&bar_pv[2 * w + (u & 1)], (uint32_t)(u >> 1) & 1u);
+        wait(&bar_pv[2 * w + (u & 1)], p_parity, k_bar(), k_parity());
         if (good) issue_s(u + 2);
       }
     }
