@@ -31,7 +31,7 @@ __host__ __device__ constexpr int chunks_of(int heads) {
 }
 
 template <int D, bool BF16, bool IL>
-__global__ void __launch_bounds__(kThreads, 10) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const __grid_constant__ RopeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kLanes = D / 8;       // lanes of a row
@@ -61,11 +61,12 @@ __global__ void __launch_bounds__(kThreads, 10) rope_kernel(const __grid_constan
                       : is_v ? static_cast<const uint16_t*>(p.v) + (size_t)t * p.vs
                              : static_cast<const uint16_t*>(p.k) + (size_t)t * p.ks;
   uint4 raw[kUnroll];
+  const uint16_t* src_a = src + row0 * D + a;
+  const uint16_t* src_b = src + row0 * D + b;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int row = row0 + u * kRows;
-    raw[u] = row < heads ? load_pairs<IL>(src + (size_t)row * D, a, b) : make_uint4(0, 0, 0, 0);
-  }
+  for (int u = 0; u < kUnroll; ++u)
+    raw[u] = row0 + u * kRows < heads ? load_pairs<IL>(src_a + u * kRows * D, src_b + u * kRows * D)
+                                      : make_uint4(0, 0, 0, 0);
   // where the rows go: heads of a token follow one another in an output, and lie
   // two tiles of a block apart in the cache
   uint16_t* dst;
@@ -81,25 +82,33 @@ __global__ void __launch_bounds__(kThreads, 10) rope_kernel(const __grid_constan
     dst = reinterpret_cast<uint16_t*>(p.cache) +
           (((size_t)(slot >> 4) * p.Hkv * 2 + (is_v ? 1 : 0)) * kBlock + (slot & 15)) * D;
   }
-  if (is_v) {
+  dst += row0 * step;
+  auto put = [&](int u, uint4 out) {
+    uint16_t* row = dst + u * kRows * step;
+    if (row0 + u * kRows < heads) store_pairs<IL>(row + a, row + b, out);
+  };
+  const float* weight = is_v ? nullptr : is_q ? p.r.q_weight : p.r.k_weight;
+  const bool turn = !is_v && 2 * i0 < p.r.rot;
+  if (!weight && p.r.rot == 0) is_v = true;  // nothing to do to them either
+  Pairs cs;
+  if (!is_v && !load_angles(p.r, pos, i0, cs)) {
+    if (lane == 0 && chunk == 0) raise_flag(p.err, PQKV_DEVERR_POSITION);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int row = row0 + u * kRows;
-      if (row < heads) store_pairs<IL>(dst + row * step, a, b, raw[u]);
-    }
+    for (int u = 0; u < kUnroll; ++u) put(u, make_uint4(0, 0, 0, 0));
     return;
   }
-  Pairs cs;
-  const bool ok = load_angles(p.r, pos, i0, cs);
-  if (!ok && lane == 0 && chunk == 0) raise_flag(p.err, PQKV_DEVERR_POSITION);
-  const float* weight = is_q ? p.r.q_weight : p.r.k_weight;
+  if (is_v) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) put(u, raw[u]);
+    return;
+  }
   Pairs w = {};
   if (weight) w = load_weight<IL>(weight, a, b);
+  const Coefficients k = coefficients<IL>(weight != nullptr, w, turn, cs);
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    const int row = row0 + u * kRows;
-    const Pairs z = norm_rotate<D>(unpack_pairs<BF16, IL>(raw[u]), weight != nullptr, w, p.r.eps, 2 * i0 < p.r.rot, cs);
-    if (row < heads) store_pairs<IL>(dst + row * step, a, b, ok ? pack_pairs<BF16, IL>(z) : make_uint4(0, 0, 0, 0));
+    const uint4 out = norm_rotate<D, BF16, IL>(raw[u], weight != nullptr, p.r.eps, k);
+    put(u, weight || turn ? out : raw[u]);
   }
 }
 

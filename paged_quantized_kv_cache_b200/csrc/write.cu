@@ -96,17 +96,18 @@ __device__ __forceinline__ void stage_run(const WriteParams& p, int ts, int n, i
     if (mine) {
       const uint16_t* src = kv ? static_cast<const uint16_t*>(p.v) + (size_t)(ts + j) * p.vs
                                : static_cast<const uint16_t*>(p.k) + (size_t)(ts + j) * p.ks;
-      raw = load_pairs<IL>(src + (size_t)h * D, a, b);
+      raw = load_pairs<IL>(src + (size_t)h * D + a, src + (size_t)h * D + b);
     }
     if (kv == 0) {
       Pairs cs = {};
       int pos[kMaxAxes];
       if (mine) load_positions(p.rope, ts + j, pos);
       const bool ok = !mine || load_angles(p.rope, pos, i0, cs);
-      const Pairs z = norm_rotate<D>(unpack_pairs<BF16, IL>(raw), norm, w, p.rope.eps, 2 * i0 < p.rope.rot, cs);
-      raw = ok ? pack_pairs<BF16, IL>(z) : make_uint4(0, 0, 0, 0);
+      const bool turn = 2 * i0 < p.rope.rot;
+      const uint4 out = norm_rotate<D, BF16, IL>(raw, norm, p.rope.eps, coefficients<IL>(norm, w, turn, cs));
+      raw = !ok ? make_uint4(0, 0, 0, 0) : norm || turn ? out : raw;
     }
-    if (mine) store_pairs<IL>(rows + j * D, a, b, raw);
+    if (mine) store_pairs<IL>(rows + j * D + a, rows + j * D + b, raw);
   }
   __syncwarp();
 }
