@@ -607,6 +607,7 @@ int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_
   p.max_q = max_q_len;
   p.tiles_per_seq = (int)tiles;
   p.splits = 1;
+  p.by_length = 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = g_decode_wait_ns.load();
   p.drain_ns = kWaitLimitNs;

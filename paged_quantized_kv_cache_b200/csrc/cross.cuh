@@ -26,6 +26,7 @@ struct CrossParams {
   int max_q;                    // query tokens of the longest sequence
   int tiles_per_seq;            // 128-row query tiles per sequence
   int splits;                   // CTAs of a cluster, which share the states of their rows (set by the launcher)
+  int by_length;                // sequences in the order of their lengths (set by the launcher)
   float scale_log2;             // softmax scale * log2(e)
   uint64_t timeout_ns;          // limit of a wait before a warp gives up
   uint64_t drain_ns;            // after giving up: limit of the wait for work still in flight

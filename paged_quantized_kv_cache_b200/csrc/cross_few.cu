@@ -45,7 +45,7 @@ struct FewGeom {
   // partial results, over the tiles and sides once the blocks are done with
   static constexpr int kPart = NC * (D + 2) * 4;  // O [NC][D], m [NC], l [NC]
   static_assert((kWarps + 1) * kPart <= kTilesBytes + kSideBytes, "the warps' and the CTA's partial results");
-  static_assert(2 * (kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
+  static_assert(2 * (kSmem + 1024 + 16) <= 227 * 1024, "two CTAs per SM (16: static)");
 };
 
 template <int KVF, int D, bool QBF16, int NT>
@@ -66,7 +66,25 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
   const int g = lane >> 2, qd = lane & 3;
   const int S = p.splits, G = p.G;
   const int rank = (int)(blockIdx.x % (unsigned)S), pair = (int)(blockIdx.x / (unsigned)S);
-  const int b = pair / p.Hkv, h = pair - b * p.Hkv;
+  int b = pair / p.Hkv;
+  const int h = pair - b * p.Hkv;
+  if (p.by_length) {
+    // more clusters than fit at once: the longest sequences first (the b-th
+    // longest is this cluster's; equal ones in order), so that none of them is
+    // left for the end
+    __shared__ int chosen;
+    int* lens = reinterpret_cast<int*>(smem);
+    if (tid < p.B) lens[tid] = p.kv_lens[tid];
+    __syncthreads();
+    if (tid < p.B) {
+      int before = 0;
+      for (int i = 0; i < p.B; ++i) before += lens[i] > lens[tid] || (lens[i] == lens[tid] && i < tid);
+      if (before == b) chosen = tid;
+    }
+    __syncthreads();
+    b = chosen;
+    __syncthreads();  // the lengths' place is a tile's
+  }
 
   const int q0 = p.cu_q[b], qn = p.cu_q[b + 1] - q0;
   const int L = p.kv_lens[b];
@@ -358,7 +376,9 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
 #pragma unroll
       for (int c = 0; c < 2; ++c) ll[nt][c] += (w[0][nt][c] + w[0][nt][c + 2]) + (w[1][nt][c] + w[1][nt][c + 2]);
     }
-    // O^T += V^T P^T, P = P_hi + P_lo (except FP4, as in the decode)
+    // O^T += V^T P^T. 16-bit caches, which the memory bounds, take P = P_hi + P_lo;
+    // the others, bound by instruction issue, P in f16 alone (2^-11 of p, far
+    // below their codes' own steps): 7% fewer instructions per FP8 block.
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!use[i] || (Gm::kFp8 && !(pr[i] > 0.f))) continue;
@@ -371,12 +391,12 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
         b0[nt] = movmatrix_t(hA);
         b1[nt] = movmatrix_t(hB);
         c0[nt] = c1[nt] = 0u;
-        if constexpr (!Gm::kFp4) {
+        if constexpr (Gm::k16) {
           c0[nt] = movmatrix_t(pack_f32x2(w0 - unpack_lo(hA, kBf16Mma), w1 - unpack_hi(hA, kBf16Mma), kBf16Mma));
           c1[nt] = movmatrix_t(pack_f32x2(w2 - unpack_lo(hB, kBf16Mma), w3 - unpack_hi(hB, kBf16Mma), kBf16Mma));
         }
       }
-      block_pv<KVF, D, NT>(tb[i], sd[i], lofs, lane, min(kBlock, L - base - kBlock * i), b0, b1, c0, c1, acc, woext, ost);
+      block_pv<KVF, D, NT, Gm::k16>(tb[i], sd[i], lofs, lane, min(kBlock, L - base - kBlock * i), b0, b1, c0, c1, acc, woext, ost);
     }
     __syncwarp();
     if (v + NS < V) issue(sA, v + NS);
@@ -505,6 +525,8 @@ cudaError_t launch_few_t(const CUtensorMap& tmap, CrossParams p, int sms, cudaSt
   }
   const long long pairs = (long long)p.B * p.Hkv;
   p.splits = few_splits(pairs, p.maxblk, Fg::kWarps, sms);
+  // a thread ranks a sequence
+  p.by_length = pairs * p.splits > 2LL * sms && p.B <= Fg::kThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pairs * p.splits));
   cfg.blockDim = dim3(Fg::kThreads);

@@ -305,7 +305,8 @@ __device__ __forceinline__ void block_scores(uint32_t tb, const uint8_t* side,
 // tile as two B fragments (hi and lo parts, P = P_hi + P_lo rounded to the
 // operand type); the V fragments are dequantized once for all tiles.
 // ---------------------------------------------------------------------------
-template <int KVF, int D, int NT>
+// SPLIT: with P_lo (FP4 keeps P in f16 only; its tolerance allows it).
+template <int KVF, int D, int NT, bool SPLIT = (KVF != PQKV_DTYPE_FP4_E2M1)>
 __device__ __forceinline__ void block_pv(uint32_t tb, const uint8_t* side, const LdsmOffsets<KVF, D>& lo, int lane,
                                          int valid, const uint32_t (&b0)[NT], const uint32_t (&b1)[NT],
                                          const uint32_t (&c0)[NT], const uint32_t (&c1)[NT],
@@ -315,8 +316,7 @@ __device__ __forceinline__ void block_pv(uint32_t tb, const uint8_t* side, const
   constexpr bool kBf = (KVF == PQKV_DTYPE_BF16);
   const int g = lane >> 2, qd = lane & 3;
   const int t0 = 2 * qd, t1 = 2 * qd + 8;
-  // FP4 keeps P in f16 only (its tolerance allows it); the others add P_lo.
-  constexpr bool kSplitP = !Gm::kFp4;
+  constexpr bool kSplitP = SPLIT;
   auto mma_pv = [&](int nt, float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
     mma16816<kBf>(d, a0, a1, a2, a3, b0[nt], b1[nt]);
     if constexpr (kSplitP) mma16816<kBf>(d, a0, a1, a2, a3, c0[nt], c1[nt]);

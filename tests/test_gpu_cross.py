@@ -158,6 +158,18 @@ def test_a_few_tokens(case, qlens):
     _check(g, o, q, cu, bt, lens, 1 / np.sqrt(case[2]), _ranges(rng, cu, lens))
 
 
+@pytest.mark.parametrize("batch", [40, 96, 97, 130, 193])
+def test_many_sequences_of_a_few_tokens(batch):
+    """More clusters than fit the GPU at once, taken in the order of their lengths (equal and empty ones among
+    them) while a thread can rank a sequence, in the batch's order beyond."""
+    case = (pq.FP8_E4M3, torch.bfloat16, 64, 8, 8)
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in rng.integers(0, 60, batch)]
+    qlens = [int(x) for x in rng.integers(0, 4, batch)]
+    g, o, bt, cu, q, lens = _build(case, lens, qlens, seed=900 + batch)
+    _check(g, o, q, cu, bt, lens, 0.125)
+
+
 def test_few_tokens_edges():
     for case in (CASES[0], CASES[5], CASES[6]):
         g, o, bt, cu, q, lens = _build(case, [100, 0, 40, 260, 17], [1, 2, 0, 2, 1], seed=607)
