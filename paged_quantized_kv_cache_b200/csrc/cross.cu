@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   const int h = blockIdx.y, rank = blockIdx.z;
   const int G = p.G, TOK = kM / G;
   const int ctas = (p.tiles_per_seq + 1) / 2;
-  const int b = blockIdx.x / ctas, mt0 = 2 * (int)(blockIdx.x % ctas);  // first row tile
+  int b = blockIdx.x / ctas;
+  const int mt0 = 2 * (int)(blockIdx.x % ctas);  // first row tile
+  if (p.by_length) b = nth_longest(p.kv_lens, p.B, b, reinterpret_cast<int*>(smem));
   const int q0 = p.cu_q[b], qn = p.cu_q[b + 1] - q0;
   const int L = p.kv_lens[b];
   if (mt0 == 0 && h == 0 && rank == 0 && tid == 0 && qn > p.tiles_per_seq * TOK)
@@ -969,6 +971,7 @@ cudaError_t launch_cross_t(const CUtensorMap& tmap, CrossParams p, int sms, cuda
   }
   const unsigned pairs = (unsigned)(p.B * ((p.tiles_per_seq + 1) / 2));
   p.splits = cross_splits((long long)pairs * p.Hkv, p.maxblk, sms);
+  p.by_length = p.B > 1 && p.B <= Gm::kThreads && (long long)pairs * p.Hkv > sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(pairs, (unsigned)p.Hkv, (unsigned)p.splits);
   cfg.blockDim = dim3(Gm::kThreads);

@@ -32,6 +32,28 @@ struct CrossParams {
   uint64_t drain_ns;            // after giving up: limit of the wait for work still in flight
 };
 
+// Index of the b-th longest of B sequences (B at most the CTA's threads: one
+// ranks a sequence; equal ones in order), in `scratch`, B + 1 words of shared
+// memory that are free again on return. Every thread of the CTA calls it. With
+// more CTAs than fit at once, those of the longest sequences start first, so
+// that none of them is left for the end: 64 sequences of 2048-6404 FP8 states,
+// one token each, 136 against 112 us.
+__device__ __forceinline__ int nth_longest(const int32_t* kv_lens, int B, int b, int* scratch) {
+  const int tid = threadIdx.x;
+  if (tid < B) scratch[tid] = kv_lens[tid];
+  __syncthreads();
+  if (tid < B) {
+    const int mine = scratch[tid];
+    int before = 0;
+    for (int i = 0; i < B; ++i) before += scratch[i] > mine || (scratch[i] == mine && i < tid);
+    if (before == b) scratch[B] = tid;
+  }
+  __syncthreads();
+  const int chosen = scratch[B];
+  __syncthreads();
+  return chosen;
+}
+
 // Tiles of 128 query rows on tcgen05 (cross.cu; the prefill's tensor map for
 // 16-bit caches), or at most kFewColumns rows per KV head (cross_few.cu; the
 // decode's tensor map).

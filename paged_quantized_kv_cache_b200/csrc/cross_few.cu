@@ -45,7 +45,7 @@ struct FewGeom {
   // partial results, over the tiles and sides once the blocks are done with
   static constexpr int kPart = NC * (D + 2) * 4;  // O [NC][D], m [NC], l [NC]
   static_assert((kWarps + 1) * kPart <= kTilesBytes + kSideBytes, "the warps' and the CTA's partial results");
-  static_assert(2 * (kSmem + 1024 + 16) <= 227 * 1024, "two CTAs per SM (16: static)");
+  static_assert(2 * (kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
 };
 
 template <int KVF, int D, bool QBF16, int NT>
@@ -68,23 +68,7 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
   const int rank = (int)(blockIdx.x % (unsigned)S), pair = (int)(blockIdx.x / (unsigned)S);
   int b = pair / p.Hkv;
   const int h = pair - b * p.Hkv;
-  if (p.by_length) {
-    // more clusters than fit at once: the longest sequences first (the b-th
-    // longest is this cluster's; equal ones in order), so that none of them is
-    // left for the end
-    __shared__ int chosen;
-    int* lens = reinterpret_cast<int*>(smem);
-    if (tid < p.B) lens[tid] = p.kv_lens[tid];
-    __syncthreads();
-    if (tid < p.B) {
-      int before = 0;
-      for (int i = 0; i < p.B; ++i) before += lens[i] > lens[tid] || (lens[i] == lens[tid] && i < tid);
-      if (before == b) chosen = tid;
-    }
-    __syncthreads();
-    b = chosen;
-    __syncthreads();  // the lengths' place is a tile's
-  }
+  if (p.by_length) b = nth_longest(p.kv_lens, p.B, b, reinterpret_cast<int*>(smem));
 
   const int q0 = p.cu_q[b], qn = p.cu_q[b + 1] - q0;
   const int L = p.kv_lens[b];
@@ -525,7 +509,6 @@ cudaError_t launch_few_t(const CUtensorMap& tmap, CrossParams p, int sms, cudaSt
   }
   const long long pairs = (long long)p.B * p.Hkv;
   p.splits = few_splits(pairs, p.maxblk, Fg::kWarps, sms);
-  // a thread ranks a sequence
   p.by_length = pairs * p.splits > 2LL * sms && p.B <= Fg::kThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(pairs * p.splits));
