@@ -622,12 +622,13 @@ int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch
                      int num_new_blocks, int32_t* block_tables, int max_blocks_per_seq, int num_blocks,
                      int max_tokens, int32_t* slot_mapping, int32_t* positions, int32_t* cu_q_lens,
                      int32_t* seq_lens, int32_t* err_flag, pqkv_stream_t stream) {
-  if (batch < 1 || batch > PQKV_MAX_BATCH || num_new_blocks < 0 || max_blocks_per_seq < 1 ||
+  if (batch < 0 || batch > PQKV_MAX_BATCH || num_new_blocks < 0 || max_blocks_per_seq < 1 ||
       max_blocks_per_seq > INT32_MAX / PQKV_BLOCK_SIZE || num_blocks < 1 || max_tokens < 0)
     return PQKV_ERR_ARG;
   if ((int64_t)num_blocks * PQKV_BLOCK_SIZE > INT32_MAX) return PQKV_ERR_ARG;
-  if (!start_pos || !num_new || (num_new_blocks > 0 && !new_block_ids) || !block_tables ||
-      (max_tokens > 0 && (!slot_mapping || !positions)) || !cu_q_lens || !seq_lens || !err_flag)
+  if ((batch > 0 && (!start_pos || !num_new || !block_tables || !seq_lens)) ||
+      (num_new_blocks > 0 && !new_block_ids) || (max_tokens > 0 && (!slot_mapping || !positions)) || !cu_q_lens ||
+      !err_flag)
     return PQKV_ERR_ARG;
   DeviceInfo di;
   if (!device_info(di)) return PQKV_ERR_CUDA;

@@ -123,12 +123,12 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const BatchParams
   __syncthreads();
 
   const int step = gridDim.x * kThreads;
-  for (int i = blockIdx.x * kThreads + tid; i < M; i += step) {
-    const int b = owner(blk, p.B, i);
+  for (long long i = (long long)blockIdx.x * kThreads + tid; i < M; i += step) {
+    const int b = owner(blk, p.B, (int)i);
     const int id = p.ids[i];
     const bool ok = id >= 0 && id < p.nb;
     if (!ok) raise_flag(p.err, PQKV_DEVERR_BLOCK_ID);
-    p.tables[(size_t)b * p.maxblk + blocks_of(p.start[b]) + (i - blk[b])] = ok ? id : -1;
+    p.tables[(size_t)b * p.maxblk + blocks_of(p.start[b]) + ((int)i - blk[b])] = ok ? id : -1;
   }
   for (long long i = (long long)blockIdx.x * kThreads + tid; i < p.cap; i += step) {
     int slot = -1, pos = 0;

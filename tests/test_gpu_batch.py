@@ -61,6 +61,10 @@ def test_no_new_tokens_anywhere():
     _check(args, 12)
 
 
+def test_no_requests():
+    _check((np.zeros(0, int), np.zeros(0, int), np.zeros(0, int), np.zeros((0, 4), int), 5), 9)
+
+
 def test_bad_lengths_leave_a_request_empty():
     args = _case(np.random.default_rng(6), 9, 50, 20)
     start, new, ids, tables, nb = args

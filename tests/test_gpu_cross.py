@@ -209,6 +209,58 @@ def test_few_tokens_wait_limit_runs_out_and_the_next_call_is_correct(case, lens)
     _check(g, o, q, cu, bt, lens, 0.088)
 
 
+def _sloped(case, L, tokens, shape, seed):
+    """Scores that run from -`top` to `top` (times a little noise) over the positions in the given shape: the row
+    max moves at every tile, by much, at one position only, or never again after the first."""
+    kv_dtype, qdt, D, Hq, Hkv = case
+    rng = np.random.default_rng(seed)
+    nb = -(-L // 16) + 1
+    bt = random_tables(rng, [L], nb)
+    g, o = gh.new_pair(kv_dtype, nb, Hkv, D)
+    at = np.linspace(-1, 1, L)
+    ramp = {"up": at, "down": -at, "spike": np.where(np.arange(L) == L - 40, 1, -0.2), "steps": np.floor(at * 3) / 3}[shape]
+    k = (ramp[:, None, None] + 0.02 * rng.standard_normal((L, Hkv, D))).astype(np.float32)
+    v = rng.standard_normal((L, Hkv, D)).astype(np.float32)
+    assert gh.write_both(g, o, torch.from_numpy(k).to(qdt), torch.from_numpy(v).to(qdt), slots(bt[0], 0, L)) == (0, 0)
+    q = torch.from_numpy((1 + 0.02 * rng.standard_normal((tokens, Hq, D))).astype(np.float32)).to(qdt)
+    return g, o, q, np.array([0, tokens], np.int32), bt
+
+
+@pytest.mark.parametrize("shape", ["up", "down", "spike", "steps"])
+@pytest.mark.parametrize("top", [6, 60, 400])
+@pytest.mark.parametrize("case", [CASES[0], CASES[1], CASES[4], CASES[6]], ids=ID)
+def test_row_maxima_that_move(case, top, shape):
+    """Exponents past what the standing max allows (2^15 for P in f16, 2^60 in bf16), in both kernels."""
+    D = case[2]
+    for tokens in (1, 70):
+        g, o, q, cu, bt = _sloped(case, 700, tokens, shape, seed=800 + tokens)
+        _check(g, o, q, cu, bt, [700], top / D)
+        r = np.tile([[100, 650]], (tokens, 1))
+        r[::3] = [0, 130]
+        _check(g, o, q, cu, bt, [700], top / D, r)
+
+
+@pytest.mark.parametrize("batch,Hkv", [(40, 8), (700, 1)])
+def test_many_sequences_of_many_rows(batch, Hkv):
+    """More CTAs than fit the GPU at once, in the order of the sequences' lengths, and past the number of
+    sequences that the threads of a CTA can rank."""
+    for kv_dtype, dtype in ((pq.BF16, torch.bfloat16), (pq.FP8_E5M2, torch.float16)):
+        case = (kv_dtype, dtype, 64, 8 * Hkv, Hkv)
+        rng = np.random.default_rng(batch)
+        lens = [int(x) for x in rng.integers(0, 90, batch)]
+        qlens = [int(x) for x in rng.integers(0, 4, batch)]
+        qlens[3] = 3
+        g, o, bt, cu, q, lens = _build(case, lens, qlens, seed=901 + batch)
+        _check(g, o, q, cu, bt, lens, 0.125)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 8.0])
+@pytest.mark.parametrize("case", [CASES[0], CASES[4]], ids=ID)
+def test_other_scales_of_many_rows(case, scale):
+    g, o, bt, cu, q, lens = _build(case, [200, 500], [30, 70], seed=605)
+    _check(g, o, q, cu, bt, lens, scale)
+
+
 def test_empty_and_rejected_sequences():
     case = CASES[1]
     lens, qlens = [40, 0, 30, 0, 20], [5, 4, 0, 1, 3]

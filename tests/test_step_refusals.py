@@ -22,7 +22,7 @@ def _batch(**kw):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(batch=0), dict(batch=pq.MAX_BATCH + 1), dict(n_ids=-1), dict(maxblk=0), dict(maxblk=1 << 28), dict(nb=0),
+    dict(batch=-1), dict(batch=pq.MAX_BATCH + 1), dict(n_ids=-1), dict(maxblk=0), dict(maxblk=1 << 28), dict(nb=0),
     dict(nb=1 << 28), dict(cap=-1), dict(start=None), dict(new=None), dict(ids=None), dict(tables=None),
     dict(slots=None), dict(pos=None), dict(cu=None), dict(lens=None), dict(err=None)], ids=str)
 def test_batch_refuses(bad):
