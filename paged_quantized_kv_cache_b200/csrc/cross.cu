@@ -109,12 +109,19 @@ struct CrossGeom {
   static_assert(2 * kM * (D * 4 + 8) <= oMisc, "partial O, m and l over the queries, stages and operands");
 };
 
+// The tcgen05 loads, stores and allocations and the named barriers want their
+// warp converged; waits and loops whose lanes may part come before many of
+// them, so each such place has a __syncwarp first.
 template <int N>
-__device__ __forceinline__ void deq_sync() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void deq_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
 
 // And-reduction over the `n` threads (a multiple of 32) of named barrier `id`.
 __device__ __forceinline__ bool bar_all(int id, int n, bool v) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
@@ -135,6 +142,7 @@ __device__ __forceinline__ float exponents(uint32_t t_s, float nm, const float (
   tc::tmem_ld16_start(t_s, x[0]);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    if constexpr (kMasked) __syncwarp();
     tc::tmem_ld_wait(x[j & 1]);
     if (j < 3) tc::tmem_ld16_start(t_s + 16 * (j + 1), x[(j + 1) & 1]);
 #pragma unroll
@@ -163,6 +171,7 @@ __device__ __forceinline__ float largest(uint32_t t_s, const float (&cj)[4], uin
   tc::tmem_ld16_start(t_s, x[0]);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
+    if constexpr (kMasked) __syncwarp();
     tc::tmem_ld_wait(x[j & 1]);
     if (j < 3) tc::tmem_ld16_start(t_s + 16 * (j + 1), x[(j + 1) & 1]);
 #pragma unroll
@@ -293,6 +302,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   auto lap_of = [&](int t) { return (uint32_t)(ns == 4 ? t >> 2 : t / 5) & 1u; };
 
   // ---- setup: tensor memory, barriers ----
+  __syncwarp();
   if (warp == 0) tc::tmem_alloc(tmem_slot, 512);
   if (tid == 32 * Gm::kProducer) {
     if constexpr (Gm::k16) prefetch_tensormap(&tmap);
@@ -756,6 +766,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
           for (int j = 0; j < 4; ++j)
             if (!((mask >> j) & 1)) cols &= ~(0xFFFFull << (16 * j));
         }
+        __syncwarp();
         const float mx = plain ? largest<false>(t_s, cj, 0) : largest<true>(t_s, cj, cols);
         float fo = 1.f;  // rescale of l and O for a larger row max
         if (mx > m + kLazy && !none) {
@@ -767,6 +778,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
           fo *= vref / top;
           vref = top;
         }
+        __syncwarp();
         if (plain)
           sum = exponents<false, Gm::kFp8, kBfMma>(t_s, none ? -INFINITY : -m, cj, vr, 0, pk);
         else
@@ -774,6 +786,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
         // O is rescaled once PV(u - 1) is done, before PV(u) is issued (which waits for P(u))
         if (u > 0 && __any_sync(kFull, fo != 1.f)) {
           ok = mbar_wait_bounded(&my_pv[(u - 1) & 1], (uint32_t)((u - 1) >> 1) & 1u, p.timeout_ns) && ok;
+          __syncwarp();
           tc::fence_after_sync();
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
@@ -792,6 +805,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
       }
       l += sum;
       // P over this row's columns of S, then the warp's share is handed over
+      __syncwarp();
       tc::tmem_st32(t_s, pk);
       tc::fence_before_sync();
       __syncwarp();
@@ -842,6 +856,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   auto leave_part = [&]() {  // this thread's channels of its row, and m and l
     const int slot = wg * kM + r;
     if (group == 0) s_stat[slot] = make_float2(m, l);
+    __syncwarp();
     if (tiles_of(wg) > 0) {
       const float vs = Gm::kFp8 ? vref : 1.f;
 #pragma unroll 1
@@ -872,6 +887,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
 #pragma unroll 1
       for (int c0 = group * (D / H); c0 < (group + 1) * (D / H); c0 += 32) {
         uint32_t o[32];
+        __syncwarp();
         tc::tmem_ld32(t_row + c0, o);
         if (!row_ok) continue;
 #pragma unroll
@@ -942,6 +958,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     cluster_sync();  // no CTA leaves while another reads its parts
   }
   if (warp == 0) {
+    __syncwarp();
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
