@@ -86,11 +86,14 @@ struct CrossGeom {
   static constexpr int kValBytes = kFp4 ? 2 * 16 * 4 * 2 : 0;
   static constexpr int kIdxBytes = kFp4 ? 16 : 0;
   static constexpr int kSide = kScaleBytes + kValBytes + kIdxBytes;
-  static constexpr int kStages = 4;                   // KV tiles in flight; 16-bit dup: one more, in the free Q tile
-  static constexpr int kMaxStages = kStages + 1;
+  // KV tiles in flight. A wait for a tile sees only the parity of its stage's
+  // phase, so whoever waits must know that the stage's tile before has landed:
+  // with an even count the halves that take the tiles in turn (dup) each keep to
+  // stages of their own, and have read that tile themselves.
+  static constexpr int kStages = 4;
+  static_assert(kStages % 2 == 0, "a stage belongs to one half");
   static constexpr int kRawStage = k16 ? 2 * kOpBytes : 4 * (kRawTile + kSide);
   static constexpr int kStageBytes = (kRawStage + 1023) / 1024 * 1024;
-  static_assert(!k16 || kStageBytes == kQBytes, "a KV tile fits a Q tile's place");
   static constexpr int kKops = k16 ? 0 : 2;           // dequantized K tiles
   static constexpr int kVops = k16 ? 0 : 3;           // dequantized V tiles
   static constexpr int kMasks = 16;                   // block masks of KV tiles t % 16
@@ -99,10 +102,13 @@ struct CrossGeom {
   static constexpr int oKop = oStage + kStages * kStageBytes;
   static constexpr int oVop = oKop + kKops * kOpBytes;
   static constexpr int oMisc = oVop + kVops * kOpBytes;
-  static constexpr int kBars = 4 * kMaxStages + 12 + 4 + 2 + 3 + 8 + 2 + 1;
-  static constexpr int oScales = oMisc + (kBars * 8 + 15) / 16 * 16;  // FP8 scales of tile t % 4: K [4][4], V [4][4]
-  static constexpr int oWords = oScales + 128;
-  static constexpr int kWords = kMasks + kMaxStages + 1 + 2 + 8 + 2 + 1;
+  static constexpr int kBars = 4 * kStages + 12 + 4 + 2 + 3 + 8 + 2 + 1;
+  // FP8 scales of tile t % 8: K [8][4], V [8][4]. Tile t is dequantized once S of
+  // tile t - 2 is done; with dup that leaves tile t - 4 of the same half unread.
+  static constexpr int kScaleSlots = 8;
+  static constexpr int oScales = oMisc + (kBars * 8 + 15) / 16 * 16;
+  static constexpr int oWords = oScales + kScaleSlots * 32;
+  static constexpr int kWords = kMasks + kStages + 1 + 2 + 8 + 2 + 1;
   static constexpr int oRows = oWords + (kWords * 4 + 15) / 16 * 16;  // H = 2: max, and sum of each group, of every row
   static constexpr int kSmem = oRows + (H == 2 ? 3 * 2 * kM * 4 : 0) + 1024;  // + alignment slack
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
@@ -194,11 +200,11 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sKop = smem + Gm::oKop;
   uint8_t* sVop = smem + Gm::oVop;
-  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + Gm::oMisc);  // [kMaxStages] tile (16-bit: its K) landed
-  uint64_t* bar_empty = bar_full + Gm::kMaxStages;                      // [kMaxStages] its stage free again
-  uint64_t* bar_vfull = bar_empty + Gm::kMaxStages;                     // 16-bit: the same for V
-  uint64_t* bar_vempty = bar_vfull + Gm::kMaxStages;
-  uint64_t* bar_s = bar_vempty + Gm::kMaxStages;  // [2][2] row tile w's S(u) computed (buffer u % 2)
+  uint64_t* bar_full = reinterpret_cast<uint64_t*>(smem + Gm::oMisc);  // [kStages] tile (16-bit: its K) landed
+  uint64_t* bar_empty = bar_full + Gm::kStages;                         // [kStages] its stage free again
+  uint64_t* bar_vfull = bar_empty + Gm::kStages;                        // 16-bit: the same for V
+  uint64_t* bar_vempty = bar_vfull + Gm::kStages;
+  uint64_t* bar_s = bar_vempty + Gm::kStages;     // [2][2] row tile w's S(u) computed (buffer u % 2)
   uint64_t* bar_p = bar_s + 4;                   // [2][2] its P(u) in tensor memory (one arrival per warp)
   uint64_t* bar_pv = bar_p + 4;                  // [2][2] its PV(u) computed
   uint64_t* bar_op = bar_pv + 4;                 // [4] quantized: operands, mask and scales of tile t ready
@@ -207,11 +213,11 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   uint64_t* bar_turn = bar_vfree + 3;            // [2][4] H = 2: tile u of these 32 rows handed over (phase u)
   uint64_t* bar_drain = bar_turn + 8;            // [2] every product an MMA warp issued has completed
   uint64_t* bar_q = bar_drain + 2;               // the Q tiles are there (one arrival per compute warp)
-  float* tile_sk = reinterpret_cast<float*>(smem + Gm::oScales);  // [4][4] FP8 K scales of tile t % 4
-  float* tile_sv = tile_sk + 16;                                  // [4][4] FP8 V scales
+  float* tile_sk = reinterpret_cast<float*>(smem + Gm::oScales);  // [kScaleSlots][4] FP8 K scales
+  float* tile_sv = tile_sk + 4 * Gm::kScaleSlots;                 // [kScaleSlots][4] FP8 V scales
   volatile int* tile_mask = reinterpret_cast<volatile int*>(smem + Gm::oWords);  // [kMasks] blocks of tile t that hold data
-  volatile int* stage_mask = tile_mask + Gm::kMasks;  // [kMaxStages] quantized: the same, of a raw stage
-  volatile int* abort_flag = stage_mask + Gm::kMaxStages;
+  volatile int* stage_mask = tile_mask + Gm::kMasks;  // [kStages] quantized: the same, of a raw stage
+  volatile int* abort_flag = stage_mask + Gm::kStages;
   volatile int* n_issued = abort_flag + 1;       // [2] tiles that the producers started
   volatile int* row_moves = n_issued + 2;        // [2][4] H = 2: how often the max of these 32 rows was moved
   int* span = const_cast<int*>(row_moves) + 8;   // [2] positions that rows of the CTA see
@@ -294,19 +300,17 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   const int consumers = one_tile ? 1 : 2;  // MMA warps that read a KV tile
   auto tiles_of = [&](int w) { return dup ? (T - w + 1) >> 1 : (one_tile && w > 0 ? 0 : T); };
   const int32_t* table = p.block_tables + (size_t)b * p.maxblk;
-  const int ns = Gm::k16 && one_tile ? Gm::kMaxStages : Gm::kStages;
-  auto stage_at = [&](int s) -> uint8_t* {
-    return s < Gm::kStages ? smem + Gm::oStage + s * Gm::kStageBytes : smem + Gm::oQ + Gm::kQBytes;
-  };
-  auto stage_of = [&](int t) { return ns == 4 ? t & 3 : t % 5; };
-  auto lap_of = [&](int t) { return (uint32_t)(ns == 4 ? t >> 2 : t / 5) & 1u; };
+  constexpr int ns = Gm::kStages;
+  auto stage_at = [&](int s) -> uint8_t* { return smem + Gm::oStage + s * Gm::kStageBytes; };
+  auto stage_of = [&](int t) { return t % ns; };
+  auto lap_of = [&](int t) { return (uint32_t)(t / ns) & 1u; };
 
   // ---- setup: tensor memory, barriers ----
   __syncwarp();
   if (warp == 0) tc::tmem_alloc(tmem_slot, 512);
   if (tid == 32 * Gm::kProducer) {
     if constexpr (Gm::k16) prefetch_tensormap(&tmap);
-    for (int s = 0; s < Gm::kMaxStages; ++s) {
+    for (int s = 0; s < Gm::kStages; ++s) {
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], Gm::k16 ? consumers : 1);  // 16-bit: each MMA warp's commit; else dequantized
       mbar_init(&bar_vfull[s], 1);
@@ -438,9 +442,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     const uint32_t base = smem_u32(smem);
     const uint32_t qa = base + Gm::oQ + (one_tile ? 0 : w) * Gm::kQBytes;
     const bool issuer = tc::elect_one();
-    auto stage_addr = [&](int s) -> uint32_t {
-      return base + (s < Gm::kStages ? Gm::oStage + s * Gm::kStageBytes : Gm::oQ + Gm::kQBytes);
-    };
+    auto stage_addr = [&](int s) -> uint32_t { return base + Gm::oStage + s * Gm::kStageBytes; };
     const uint64_t q_desc = tc::sw128_desc(qa, 16, 1024);
     auto issue_s = [&](int u) {
       tc::fence_after_sync();
@@ -589,8 +591,8 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
           if (dq < 4) {
             const bool okb = (mask >> dq) & 1;
             const float* sc = reinterpret_cast<const float*>(st + 4 * Gm::kRawTile + dq * Gm::kSide);
-            tile_sk[(t & 3) * 4 + dq] = okb ? sc[0] : 0.f;
-            tile_sv[(t & 3) * 4 + dq] = okb ? sc[1] : 0.f;
+            tile_sk[(t % Gm::kScaleSlots) * 4 + dq] = okb ? sc[0] : 0.f;
+            tile_sv[(t % Gm::kScaleSlots) * 4 + dq] = okb ? sc[1] : 0.f;
           }
         }
         if (dq == 0) tile_mask[t % Gm::kMasks] = mask;
@@ -700,8 +702,8 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
       }
       float top = vref;  // FP8: the largest V scale so far, this tile's included (the same on every thread)
       if constexpr (Gm::kFp8) {
-        const float4 k4 = *reinterpret_cast<const float4*>(tile_sk + (t & 3) * 4);
-        const float4 v4 = *reinterpret_cast<const float4*>(tile_sv + (t & 3) * 4);
+        const float4 k4 = *reinterpret_cast<const float4*>(tile_sk + (t % Gm::kScaleSlots) * 4);
+        const float4 v4 = *reinterpret_cast<const float4*>(tile_sv + (t % Gm::kScaleSlots) * 4);
         const float k[4] = {k4.x, k4.y, k4.z, k4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -816,6 +818,9 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     }
 
     if (!aborted && U > 0) {
+      // PV(U - 2) first: a group whose last tile that is knows of PV(U - 4) only,
+      // and the parity that it then waits for is that of PV(U - 3) done
+      if (U > 1) ok = mbar_wait_bounded(&my_pv[U & 1], (uint32_t)((U - 2) >> 1) & 1u, p.timeout_ns) && ok;
       ok = mbar_wait_bounded(&my_pv[(U - 1) & 1], (uint32_t)((U - 1) >> 1) & 1u, p.timeout_ns) && ok;
       aborted = !__all_sync(kFull, ok);
     }

@@ -356,3 +356,19 @@ def test_wait_limit_runs_out_and_the_next_call_is_correct(case):
         pq.set_decode_wait_limit_ns(0)
     assert seen
     _check(g, o, q, cu, bt, lens, 0.088)
+
+
+@pytest.mark.parametrize("case", [CASES[0], CASES[1], CASES[4], CASES[6]], ids=ID)
+def test_the_halves_of_a_row_tile_give_the_same_bits_from_cold_memory(case):
+    # one row tile, whose halves take the KV tiles in turn, while the copies' latencies differ
+    G = case[3] // case[4]
+    lens = [1450 - 7 * b for b in range(16)]
+    qlens = [32 // G] * 16
+    g, o, bt, cu, q, lens = _build(case, lens, qlens, seed=91)
+    _check(g, o, q, cu, bt, lens, 0.1)
+    first = _run(g, q, cu, bt, lens, 0.1)[0]
+    sweep = torch.empty(64 << 20, dtype=torch.int32, device="cuda")
+    for i in range(12):
+        sweep.fill_(i)
+        out, err = _run(g, q, cu, bt, lens, 0.1)
+        assert err == 0 and torch.equal(out.view(torch.int16), first.view(torch.int16))
