@@ -343,8 +343,10 @@ int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_
  * a zero row. Rows of q behind cu_q_lens[batch] are not touched. Other
  * arguments, results and errors as in pqkv_paged_prefill_attention (a
  * kv_lens[b] below 0 or above 16 * max_blocks_per_seq gives zero rows and
- * PQKV_DEVERR_SEQ_LEN). One kernel on `stream`, on the tensor cores (tcgen05);
- * no workspace. With one token in each of `batch` sequences and no ranges
+ * PQKV_DEVERR_SEQ_LEN). P is rounded to 16 bits for its product with V (fp32
+ * sums). max_q_len chooses between two kernels: up to 16 query rows (tokens x
+ * heads) per KV head the decode's way with a block, above that tcgen05 tiles of
+ * 128 rows. One kernel on `stream`; no workspace. batch = 0 does nothing. With one token in each of `batch` sequences and no ranges
  * pqkv_paged_decode_attention computes the same.
  */
 int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,
@@ -420,7 +422,8 @@ int pqkv_swap_in(void* cache, void* scales, void* outliers_idx, void* outliers_v
  * no blocks and seq_lens 0. An id outside [0, num_blocks), in new_block_ids or
  * in the table entry of a request's open block, sets PQKV_DEVERR_BLOCK_ID; its
  * tokens get slot -1 and a new one's table entry is -1. A table row belongs to
- * one request; the arrays must not overlap. batch <= PQKV_MAX_BATCH. One kernel
+ * one request; the arrays must not overlap. batch <= PQKV_MAX_BATCH; with batch =
+ * 0 only the padding and cu_q_lens[0] are written. One kernel
  * on `stream`; no workspace.
  */
 int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch,

@@ -34,9 +34,16 @@
 // tile again.
 //
 // P is rounded once to the operand type (f16 2^-11, bf16 2^-8 of its value: the
-// weights of a mean, whose 16-bit result is rounded as much itself); P_hi + P_lo
-// as in the prefill costs half as many products again (16 sequences of 300-512
-// tokens over 3203-6404 bf16 states: 697 against 616 us).
+// weights of a mean, whose 16-bit result is rounded as much itself): P_hi + P_lo
+// as in the prefill would be half as many products again.
+//
+// Measured (16 sequences of 300-512 tokens over 3203-6404 bf16 states, 32 / 8
+// heads of 128): 547 us, 936 TFLOP/s, when every token sees all states; 527-565 us
+// with ranges that leave 37% of them visible (a CTA walks the tiles from the
+// first to the last position that any of its rows sees). 8 sequences of 129-512 tokens over 1000-4096
+// FP4 states: 190 us, 565 TFLOP/s. With 16-bit caches the tensor pipe bounds it: S of 64
+// columns reads shared memory for most of a tile pair's time (about 1376 of
+// 1700 cycles). Quantized caches: the softmax of 8 warps, 2300 cycles a tile.
 //
 // FP8 scales stay out of the operands: the K scale of a block multiplies its
 // scores, the V scale P relative to the largest so far (O is kept in units of
@@ -226,6 +233,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   float* row_sum = row_max + 2 * kM;                            // [2 groups][2][128] H = 2
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // 4 sequences of 3-40 tokens: 11.7 -> 11.4 us
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same register for the whole warp
   const int h = blockIdx.y, rank = blockIdx.z;
@@ -345,7 +353,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     // ================= producers: KV tiles (16-bit: K, and V) into the stage rings =================
     // A lane per copy of a tile (copy `what` of block j), its block ids read two
     // tiles ahead: read and issued one after the other by one thread, a tile
-    // took 1450 cycles, twice what a decode step's tile takes to arrive.
+    // took 1450 cycles.
     constexpr int kCopies = Gm::k16 ? Gm::NB : (Gm::kFp8 ? 2 : 4);  // per block
     const int kv = warp - Gm::kProducer;  // 16-bit: 0 = K, 1 = V
     uint64_t* full = kv ? bar_vfull : bar_full;
@@ -970,7 +978,9 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
 }
 
 // CTAs per row-tile pair: doubled while the doubled grid still fits the GPU at
-// one CTA per SM and every CTA keeps two tiles, one for each of its halves.
+// one CTA per SM and every CTA keeps two tiles, one for each of its halves
+// (4 sequences of 3-40 tokens over 1-577 states: 12.2 us; 12.7 without splits,
+// 14.5 and 17.5 when a CTA keeps four and eight tiles).
 int cross_splits(long long ctas, int maxblk, int sms) {
   const int tiles = (maxblk * kBlock + kN - 1) / kN;
   int s = 1;

@@ -15,6 +15,10 @@
 // distributed shared memory, always in the same order: no workspace, one
 // launch, results that do not depend on timing. Two CTAs fit an SM, so one's
 // start and end hide behind the other's stream.
+//
+// Measured (32 / 8 heads of 128, one token each): 64 sequences of 2048-6404
+// states bf16 164 us (6.75 TB/s), FP8 106-112 us (5.0-5.3 TB/s, bound by the
+// dequantization's instructions); 16 of 1400-1500 bf16 states 20.9 us.
 #include <atomic>
 #include <climits>
 
@@ -56,6 +60,7 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
   constexpr int NC = Fg::NC, NW = Fg::kWarps, NS = Fg::kStages, KT = D / 16;
   constexpr bool kBf16Mma = (KVF == PQKV_DTYPE_BF16);
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // calls in a row, 64 x 4226 FP8 states: 111.7 -> 105.6 us
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sides = smem + Fg::kTilesBytes;
@@ -362,7 +367,8 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
     }
     // O^T += V^T P^T. 16-bit caches, which the memory bounds, take P = P_hi + P_lo;
     // the others, bound by instruction issue, P in f16 alone (2^-11 of p, far
-    // below their codes' own steps): 7% fewer instructions per FP8 block.
+    // below their codes' own steps): 64 sequences of 2048-6404 FP8 states, one
+    // token each, 144 against 136 us.
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!use[i] || (Gm::kFp8 && !(pr[i] > 0.f))) continue;

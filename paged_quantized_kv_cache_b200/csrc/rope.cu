@@ -15,6 +15,10 @@
 // one token, all of one kind (queries, keys or values: blockIdx.y): their loads
 // are all in flight before the first sum, and the token's positions, cosines
 // and sines and the kind's weights are read once for them.
+//
+// Measured (8191 tokens, 32 / 8 heads of 128, three axes): 36.3 us, of which the
+// bytes at copy speed are 26.2; 27.3 without norm and rotation, 29.3 with the
+// norm only, 32.9 with one axis: the rest is the reading of the angles.
 #include "rope.cuh"
 
 namespace pqkv {
