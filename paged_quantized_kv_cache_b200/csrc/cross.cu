@@ -776,8 +776,10 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
           for (int j = 0; j < 4; ++j)
             if (!((mask >> j) & 1)) cols &= ~(0xFFFFull << (16 * j));
         }
-        __syncwarp();
-        const float mx = plain ? largest<false>(t_s, cj, 0) : largest<true>(t_s, cj, cols);
+        // a row that sees nothing of a plain tile goes by its mask: 0 x a key's NaN
+        // or infinity is what brought it here
+        const bool whole = __all_sync(kFull, plain && !none);
+        const float mx = whole ? largest<false>(t_s, cj, 0) : largest<true>(t_s, cj, cols);
         float fo = 1.f;  // rescale of l and O for a larger row max
         if (mx > m + kLazy && !none) {
           fo = ex2(m - mx);  // 0 when m was -inf
@@ -789,8 +791,8 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
           vref = top;
         }
         __syncwarp();
-        if (plain)
-          sum = exponents<false, Gm::kFp8, kBfMma>(t_s, none ? -INFINITY : -m, cj, vr, 0, pk);
+        if (whole)
+          sum = exponents<false, Gm::kFp8, kBfMma>(t_s, -m, cj, vr, 0, pk);
         else
           sum = exponents<true, Gm::kFp8, kBfMma>(t_s, m == -INFINITY ? 0.f : -m, cj, vr, cols, pk);
         // O is rescaled once PV(u - 1) is done, before PV(u) is issued (which waits for P(u))

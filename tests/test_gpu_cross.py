@@ -254,6 +254,22 @@ def test_many_sequences_of_many_rows(batch, Hkv):
         _check(g, o, q, cu, bt, lens, 0.125)
 
 
+@pytest.mark.parametrize("tokens", [2, 24, 70])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("case", [CASES[0], CASES[1], CASES[3]], ids=ID)
+def test_keys_that_a_token_does_not_see_may_hold_anything(case, value, tokens):
+    kv_dtype, qdt, D, Hq, Hkv = case
+    g, o, bt, cu, q, lens = _build(case, [640], [tokens], seed=17)
+    ranges = np.array([[0, 320] if t % 2 else [320, 640] for t in range(tokens)], np.int32)
+    want, tol = ref.cross(o, q, cu, bt, lens, 0.1, ranges)
+    keys = g.cache.view(qdt).view(g.num_blocks, Hkv, 2, 16, D)
+    for p in (0, 17, 319):  # positions that tokens of the second range do not see
+        keys[int(bt[0, p // 16]), :, 0, p % 16] = value
+    out, err = _run(g, q, cu, bt, lens, 0.1, ranges)
+    assert err == 0
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol)[::2].all()
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 8.0])
 @pytest.mark.parametrize("case", [CASES[0], CASES[4]], ids=ID)
 def test_other_scales_of_many_rows(case, scale):
