@@ -424,7 +424,7 @@ int pqkv_swap_in(void* cache, void* scales, void* outliers_idx, void* outliers_v
  * no blocks and seq_lens 0. An id outside [0, num_blocks), in new_block_ids or
  * in the table entry of a request's open block, sets PQKV_DEVERR_BLOCK_ID; its
  * tokens get slot -1 and a new one's table entry is -1. A table row belongs to
- * one request; the arrays must not overlap. batch <= PQKV_MAX_BATCH; with batch =
+ * one request. An output that overlaps another array -> PQKV_ERR_ARG. batch <= PQKV_MAX_BATCH; with batch =
  * 0 only the padding and cu_q_lens[0] are written. One kernel
  * on `stream`; no workspace.
  */

@@ -630,6 +630,17 @@ int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch
       (num_new_blocks > 0 && !new_block_ids) || (max_tokens > 0 && (!slot_mapping || !positions)) || !cu_q_lens ||
       !err_flag)
     return PQKV_ERR_ARG;
+  // every CTA reads the inputs while others write the outputs: none shares memory with another
+  const struct {
+    const void* p;
+    size_t n;
+  } arrays[8] = {{block_tables, (size_t)batch * max_blocks_per_seq}, {slot_mapping, (size_t)max_tokens},
+                 {positions, (size_t)max_tokens}, {cu_q_lens, (size_t)batch + 1}, {seq_lens, (size_t)batch},
+                 {start_pos, (size_t)batch}, {num_new, (size_t)batch}, {new_block_ids, (size_t)num_new_blocks}};
+  for (int i = 0; i < 5; ++i)  // the first five are outputs
+    for (int j = i + 1; j < 8; ++j)
+      if (arrays[i].n && arrays[j].n && overlap(arrays[i].p, 4 * arrays[i].n, arrays[j].p, 4 * arrays[j].n))
+        return PQKV_ERR_ARG;
   DeviceInfo di;
   if (!device_info(di)) return PQKV_ERR_CUDA;
   BatchParams p;

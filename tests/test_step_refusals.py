@@ -15,7 +15,8 @@ A = 1 << 20  # stands for an aligned device pointer: every call below is refused
 
 
 def _batch(**kw):
-    a = dict(start=A, new=A, batch=4, ids=A, n_ids=3, tables=A, maxblk=8, nb=64, cap=10, slots=A, pos=A, cu=A, lens=A, err=A)
+    a = dict(start=A, new=2 * A, batch=4, ids=3 * A, n_ids=3, tables=4 * A, maxblk=8, nb=64, cap=10, slots=5 * A,
+             pos=6 * A, cu=7 * A, lens=8 * A, err=9 * A)
     a.update(kw)
     return pq.lib().pqkv_build_batch(a["start"], a["new"], a["batch"], a["ids"], a["n_ids"], a["tables"], a["maxblk"],
                                      a["nb"], a["cap"], a["slots"], a["pos"], a["cu"], a["lens"], a["err"], None)
@@ -24,9 +25,18 @@ def _batch(**kw):
 @pytest.mark.parametrize("bad", [
     dict(batch=-1), dict(batch=pq.MAX_BATCH + 1), dict(n_ids=-1), dict(maxblk=0), dict(maxblk=1 << 28), dict(nb=0),
     dict(nb=1 << 28), dict(cap=-1), dict(start=None), dict(new=None), dict(ids=None), dict(tables=None),
-    dict(slots=None), dict(pos=None), dict(cu=None), dict(lens=None), dict(err=None)], ids=str)
+    dict(slots=None), dict(pos=None), dict(cu=None), dict(lens=None), dict(err=None),
+    dict(lens=A), dict(cu=A - 16), dict(slots=2 * A + 12), dict(tables=3 * A - 124), dict(pos=5 * A + 36),
+    dict(lens=7 * A + 16)], ids=str)
 def test_batch_refuses(bad):
     assert _batch(**bad) == pq.ERR_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the arguments are addresses that no kernel may see")
+@pytest.mark.parametrize("good", [dict(), dict(cu=A - 20), dict(slots=2 * A + 16), dict(ids=None, n_ids=0), dict(new=A)],
+                         ids=str)
+def test_batch_takes_arrays_side_by_side(good):
+    assert _batch(**good) == pq.ERR_CUDA  # past the checks: there is no device
 
 
 def _rope(write=False, **kw):
