@@ -691,8 +691,10 @@ int pqkv_qk_norm_rope(const void* q, const void* k, int dtype, int num_tokens, i
   p.Hq = num_q_heads;
   p.Hkv = num_kv_heads;
   p.kinds = num_kv_heads > 0 ? 1 : 0;
+  DeviceInfo di;
+  if (!device_info(di)) return PQKV_ERR_CUDA;
   const cudaError_t e =
-      launch_rope(dtype == PQKV_DTYPE_BF16, D, interleaved != 0, p, reinterpret_cast<cudaStream_t>(stream));
+      launch_rope(dtype == PQKV_DTYPE_BF16, D, interleaved != 0, p, di.sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PQKV_OK : PQKV_ERR_CUDA;
 }
 
@@ -739,7 +741,9 @@ int pqkv_qkv_norm_rope_write(const void* q, const void* k, const void* v, int dt
   p.Hkv = num_kv_heads;
   p.nb = num_blocks;
   p.kinds = is_16(kv_dtype) ? 2 : 0;
-  cudaError_t e = launch_rope(dtype == PQKV_DTYPE_BF16, D, interleaved != 0, p, st);
+  DeviceInfo di;
+  if (!device_info(di)) return PQKV_ERR_CUDA;
+  cudaError_t e = launch_rope(dtype == PQKV_DTYPE_BF16, D, interleaved != 0, p, di.sms, st);
   if (e == cudaSuccess && !is_16(kv_dtype)) {
     WriteParams w;
     std::memset(&w, 0, sizeof(w));

@@ -34,7 +34,7 @@ struct RopeParams {
   int kinds;             // 0: queries only, 1: and keys, 2: and values
 };
 
-cudaError_t launch_rope(bool bf16, int D, bool interleaved, const RopeParams& p, cudaStream_t st);
+cudaError_t launch_rope(bool bf16, int D, bool interleaved, const RopeParams& p, int sms, cudaStream_t st);
 
 // Channels of pair i of a row of D channels whose first ROT are rotated. Half
 // style: i and i + ROT / 2; interleaved: 2i and 2i + 1. The channels behind

@@ -224,3 +224,54 @@ def test_captured_and_on_another_stream():
     k_rows = lambda t: t.view(8, 2, 2, 16, 64)[:3, :, 0]  # noqa: E731
     assert (k_rows(c.cache) == k_rows(cache)).float().mean() > 0.9
     assert int(err.item()) == 0
+
+
+# T, Hq, Hkv, D, interleaved: enough rows that a warp takes two, and four, groups of them; head counts that end inside a group
+GROUPS = [(330, 250, 9, 128, False), (650, 250, 9, 128, True), (650, 245, 33, 128, False), (1400, 250, 17, 64, True),
+          (340, 250, 50, 64, False)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("case", GROUPS, ids=lambda c: "-".join(str(x) for x in c))
+def test_many_rows_give_the_bits_of_few(case, dtype):
+    """One call of many tokens, in place too, and calls of 20 tokens each; a bad position among them; with the write."""
+    T, Hq, Hkv, D, il = case
+    rot, axes = D - 8, 3
+    x, w, pos, ax, table = _make(T, Hq, Hkv, D, dtype, rot, axes, seed=31)
+    pos[1, T // 2] = -7
+    gx, gp, rotary = x.cuda(), torch.from_numpy(pos).cuda(), pq.Rotary(table.cuda(), ax, il)
+    q, k, v = _views(gx, Hq, Hkv, D)
+    kw = dict(q_weight=w[0].cuda(), k_weight=w[1].cuda())
+    new = lambda n, h: torch.full((n, h, D), float("nan"), dtype=dtype, device="cuda")  # noqa: E731
+    qa, ka, err = new(T, Hq), new(T, Hkv), gh.err_flag()
+    pq.qk_norm_rope(q, k, gp, rotary, qa, ka, err, **kw)
+    qi, ki = q.contiguous(), k.contiguous()
+    pq.qk_norm_rope(qi, ki, gp, rotary, qi, ki, err, **kw)
+    qb, kb = new(T, Hq), new(T, Hkv)
+    for t in range(0, T, 20):
+        n = slice(t, min(T, t + 20))
+        pq.qk_norm_rope(q[n], k[n], gp[:, n].contiguous(), rotary, qb[n], kb[n], err, **kw)
+    cache = pq.allocate_cache(DT[dtype], -(-T // 16), Hkv, D, fill=gh.POISON)
+    qc, slots = new(T, Hq), torch.randperm(T, generator=torch.Generator().manual_seed(1)).int().cuda()
+    pq.qkv_norm_rope_write(q, k, v, gp, rotary, qc, slots, cache, err, **kw)
+    torch.cuda.synchronize()
+    assert int(err.item()) == pq.DEVERR_POSITION
+    bits = lambda t: t.contiguous().view(torch.int16)  # noqa: E731
+    for got, want in ((qa, qb), (ka, kb), (qi, qb), (ki, kb), (qc, qb)):
+        assert torch.equal(bits(got), bits(want))
+    rows = cache.cache.view(dtype).view(-1, Hkv, 2, 16, D).permute(0, 3, 1, 2, 4).reshape(-1, Hkv, 2, D)[slots.long()]
+    assert torch.equal(bits(rows[:, :, 0]), bits(kb)) and torch.equal(bits(rows[:, :, 1]), bits(v))
+    pick = [0, 1, T // 2, T - 1]
+    _close(qa[pick], _views(x, Hq, Hkv, D)[0][pick], w[0], 1e-6, pos[:, pick], ax, table, il)
+    _close(ka[pick], _views(x, Hq, Hkv, D)[1][pick], w[1], 1e-6, pos[:, pick], ax, table, il)
+
+
+@pytest.mark.parametrize("case", GROUPS[:2], ids=lambda c: "-".join(str(x) for x in c))
+def test_many_rows_without_norm_and_rotation_are_copied(case):
+    T, Hq, Hkv, D, il = case
+    x = _make(T, Hq, Hkv, D, torch.bfloat16, 0, 1, seed=32)[0].cuda()
+    q, k, _ = _views(x, Hq, Hkv, D)
+    qo, ko = (torch.empty(T, h, D, dtype=x.dtype, device="cuda") for h in (Hq, Hkv))
+    pq.qk_norm_rope(q, k, None, None, qo, ko, gh.err_flag())
+    torch.cuda.synchronize()
+    assert torch.equal(qo, q) and torch.equal(ko, k)
