@@ -10,11 +10,12 @@
 //
 // One launch, no workspace: every CTA sums the lengths of all requests into
 // shared memory for itself (at most 4096 pairs, from L2), then the CTAs share
-// out the rows and the new blocks, a thread finding its request by bisection.
+// out the rows and the new blocks, a thread finding the request of its first row
+// by bisection.
 // A row reads its block id from the id list, or from the one table entry that
 // holds the request's open block (which no thread writes), so no CTA waits for
-// another's table entries. Latency bounds it: 2.3 us on the device for 16
-// requests of one token, 7.5 us for 512 prompts (2.8 MB of results).
+// another's table entries. Latency bounds it: 2.8 us on the device for 16
+// requests of one token, 5.6 us for 512 prompts (2.8 MB of results).
 #include "batch.cuh"
 
 namespace pqkv {
@@ -47,6 +48,8 @@ __device__ __forceinline__ int owner(const int* cum, int B, int i) {
   return lo;
 }
 
+// ROWS: consecutive rows of the batch that a thread takes, from one bisection on.
+template <int ROWS>
 __global__ void __launch_bounds__(kThreads) build_batch_kernel(const BatchParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -61,6 +64,7 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const BatchParams
 
   // sums in 64 bits: 4096 requests of up to 2^31 tokens
   long long t = 0, m = 0;
+#pragma unroll 4
   for (int i = lo; i < hi; ++i) {
     int s, n;
     lengths(p, i, s, n);
@@ -94,7 +98,8 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const BatchParams
   // Requests fit from the first one up to the one whose rows or blocks pass
   // what there is; it and all behind it are left out whole (both sums only
   // grow, so whether a request fits needs no other thread's answer).
-  int bits = 0;
+  int bits = 0, my_tok = 0, my_blk = 0;
+#pragma unroll 4
   for (int i = lo; i < hi; ++i) {
     int s, n;
     if (!lengths(p, i, s, n)) bits |= PQKV_DEVERR_SEQ_LEN;
@@ -105,12 +110,18 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const BatchParams
     tok[i + 1] = fits ? (int)t : -1;
     blk[i + 1] = fits ? (int)m : -1;
     if (fits) {
-      atomicMax(&total_tok, (int)t);
-      atomicMax(&total_blk, (int)m);
+      my_tok = (int)t;
+      my_blk = (int)m;
     }
     if (blockIdx.x == 0) p.lens[i] = fits ? s + n : 0;
   }
   if (bits && blockIdx.x == 0) raise_flag(p.err, bits);
+  my_tok = __reduce_max_sync(kFull, my_tok);
+  my_blk = __reduce_max_sync(kFull, my_blk);
+  if (lane == 0) {
+    atomicMax(&total_tok, my_tok);
+    atomicMax(&total_blk, my_blk);
+  }
   __syncthreads();
   const int T = total_tok, M = total_blk;
   for (int i = lo; i < hi; ++i) {
@@ -131,28 +142,46 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const BatchParams
     if (!ok) raise_flag(p.err, PQKV_DEVERR_BLOCK_ID);
     p.tables[(size_t)b * p.maxblk + blocks_of(p.start[b]) + ((int)i - blk[b])] = ok ? id : -1;
   }
-  for (long long i = (long long)blockIdx.x * kThreads + tid; i < p.cap; i += step) {
-    int slot = -1, pos = 0;
-    if (i < T) {
-      const int b = owner(tok, p.B, (int)i);
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15u) == 0;
+  for (long long i0 = ((long long)blockIdx.x * kThreads + tid) * ROWS; i0 < p.cap;
+       i0 += (long long)step * ROWS) {
+    int slot[ROWS], pos[ROWS];
+    int b = i0 < T ? owner(tok, p.B, (int)i0) : 0;
+#pragma unroll
+    for (int e = 0; e < ROWS; ++e) {
+      slot[e] = -1;
+      pos[e] = 0;
+      const int i = (int)min(i0 + e, (long long)T);
+      if (i >= T) continue;
+      if (e > 0)
+        while (i >= tok[b + 1]) ++b;  // tok[B] = T
       const int s = p.start[b];
-      pos = s + ((int)i - tok[b]);
-      const int j = pos / kBlock, have = blocks_of(s);
+      pos[e] = s + (i - tok[b]);
+      const int j = pos[e] / kBlock, have = blocks_of(s);
       const int id = j < have ? p.tables[(size_t)b * p.maxblk + j] : p.ids[blk[b] + j - have];
       if (id >= 0 && id < p.nb)
-        slot = id * kBlock + pos % kBlock;
+        slot[e] = id * kBlock + pos[e] % kBlock;
       else
         raise_flag(p.err, PQKV_DEVERR_BLOCK_ID);
     }
-    p.slots[i] = slot;
-    p.positions[i] = pos;
+    if (ROWS == 4 && wide && i0 + ROWS <= p.cap) {
+      *reinterpret_cast<int4*>(p.slots + i0) = make_int4(slot[0], slot[1 % ROWS], slot[2 % ROWS], slot[3 % ROWS]);
+      *reinterpret_cast<int4*>(p.positions + i0) = make_int4(pos[0], pos[1 % ROWS], pos[2 % ROWS], pos[3 % ROWS]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < ROWS; ++e)
+        if (i0 + e < p.cap) {
+          p.slots[i0 + e] = slot[e];
+          p.positions[i0 + e] = pos[e];
+        }
+    }
   }
 }
 
-}  // namespace
-
-cudaError_t launch_build_batch(const BatchParams& p, int sms, cudaStream_t st) {
-  const long long items = p.cap > p.n_ids ? p.cap : p.n_ids;
+template <int ROWS>
+cudaError_t launch_rows(const BatchParams& p, int sms, cudaStream_t st) {
+  const long long rows = ((long long)p.cap + ROWS - 1) / ROWS;
+  const long long items = rows > p.n_ids ? rows : p.n_ids;
   const long long need = (items + kThreads - 1) / kThreads;
   const int grid = (int)(need < 1 ? 1 : need < 4LL * sms ? need : 4LL * sms);
   cudaLaunchConfig_t cfg = {};
@@ -165,8 +194,20 @@ cudaError_t launch_build_batch(const BatchParams& p, int sms, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, build_batch_kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, build_batch_kernel<ROWS>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+// Four rows a thread where one each would make a second round of the CTAs that
+// fit, or the CTAs' sums of many lengths (a CTA sums all B) would take as long;
+// us with one and four: 16 rows 2.9 / 3.9, 96 requests of 25 thousand rows 3.8 /
+// 4.5, 200 of 102 thousand 4.2 / 4.8, 400 of 205 thousand 7.3 / 5.3, 512 of 328
+// thousand 8.6 / 5.6; 4096 requests of 4 thousand rows 17.5 / 19.1, of 82
+// thousand 30.8 / 18.2, of 133 thousand 52.7 / 18.2.
+cudaError_t launch_build_batch(const BatchParams& p, int sms, cudaStream_t st) {
+  return p.cap * (1 + p.B / 512.0) > 4.0 * sms * kThreads ? launch_rows<4>(p, sms, st) : launch_rows<1>(p, sms, st);
 }
 
 }  // namespace pqkv

@@ -126,3 +126,29 @@ def test_another_stream():
     got, want = _run(*args, T, stream=stream), ref.batch(*args, T)
     for g, w in zip(got, want):
         np.testing.assert_array_equal(g, w)
+
+
+@pytest.mark.parametrize("shift", [0, 1, 2, 3])
+@pytest.mark.parametrize("left", [0, 1, 2, 3, 700])
+def test_many_rows_in_arrays_of_any_alignment(shift, left):
+    """Several rows a thread: results that start on any word, rows left over, empty requests, bad ids, padding."""
+    rng = np.random.default_rng(40 + left)
+    start, new, ids, tables, nb = _case(rng, 3000, 60, 70)
+    new[rng.random(3000) < 0.3] = 0
+    need = int((-(-(start + new) // 16) - -(-start // 16)).sum())
+    ids = np.array(ids)[:need]
+    ids[[0, need // 2, need - 1]] = nb, -1, nb + 7
+    T = int(new.sum())
+    cap = T + left
+    room = [torch.full((cap + 8,), 77, dtype=torch.int32, device="cuda") for _ in range(2)]
+    slots, positions = (r[shift:shift + cap] for r in room)
+    t, cu, lens = _i32(tables).cuda(), torch.empty(3001, dtype=torch.int32, device="cuda"), torch.empty(3000, dtype=torch.int32, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pq.build_batch(_i32(start).cuda(), _i32(new).cuda(), _i32(ids).cuda(), t, nb, slots, positions, cu, lens, err)
+    torch.cuda.synchronize()
+    want = ref.batch(start, new, ids, tables, nb, cap)
+    for got, w in zip((t, slots, positions, cu, lens), want):
+        np.testing.assert_array_equal(got.cpu().numpy(), w)
+    assert int(err.item()) == want[5] == ref.ERR_BLOCK_ID
+    for r in room:
+        assert (r[:shift] == 77).all() and (r[shift + cap:] == 77).all()
