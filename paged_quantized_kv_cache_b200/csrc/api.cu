@@ -568,7 +568,7 @@ int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_
   const bool few = (int64_t)max_q_len * G <= kFewColumns;
   const int64_t tiles = ((int64_t)max_q_len * G + 127) / 128;
   // grids and TMA row coordinates fit 32 bits
-  if (tiles * batch > INT32_MAX || (int64_t)batch * num_kv_heads >= INT32_MAX / 16) return PQKV_ERR_ARG;
+  if (tiles * batch > INT32_MAX / num_kv_heads || (int64_t)batch * num_kv_heads >= INT32_MAX / 16) return PQKV_ERR_ARG;
   if ((few || is_16(kv_dtype)) && (int64_t)num_blocks * num_kv_heads * 32 >= INT32_MAX) return PQKV_ERR_ARG;
   if (batch == 0) return PQKV_OK;
   if (!q || !cu_q_lens || !cache || !block_tables || !kv_lens || !out || !err_flag) return PQKV_ERR_ARG;

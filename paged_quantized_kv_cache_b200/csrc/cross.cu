@@ -41,7 +41,8 @@
 // heads of 128): 547 us, 936 TFLOP/s, when every token sees all states; 527-565 us
 // with ranges that leave 37% of them visible (a CTA walks the tiles from the
 // first to the last position that any of its rows sees). 8 sequences of 129-512 tokens over 1000-4096
-// FP4 states: 190 us, 565 TFLOP/s. With 16-bit caches the tensor pipe bounds it: S of 64
+// FP4 states: 172 us, 624 TFLOP/s (190 us with the heads as the grid's slow
+// axis, where the last head's longest sequences start late). With 16-bit caches the tensor pipe bounds it: S of 64
 // columns reads shared memory for most of a tile pair's time (about 1376 of
 // 1700 cycles). Quantized caches: the softmax of 8 warps, 2300 cycles a tile.
 //
@@ -236,11 +237,12 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // 4 sequences of 3-40 tokens: 11.7 -> 11.4 us
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);  // the same register for the whole warp
-  const int h = blockIdx.y, rank = blockIdx.z;
+  const int h = blockIdx.x % (unsigned)p.Hkv, rank = blockIdx.z;  // all heads of the longest sequence first
   const int G = p.G, TOK = kM / G;
   const int ctas = (p.tiles_per_seq + 1) / 2;
-  int b = blockIdx.x / ctas;
-  const int mt0 = 2 * (int)(blockIdx.x % ctas);  // first row tile
+  const int pair = blockIdx.x / (unsigned)p.Hkv;
+  int b = pair / ctas;
+  const int mt0 = 2 * (pair % ctas);  // first row tile
   if (p.by_length) b = nth_longest(p.kv_lens, p.B, b, reinterpret_cast<int*>(smem));
   const int q0 = p.cu_q[b], qn = p.cu_q[b + 1] - q0;
   const int L = p.kv_lens[b];
@@ -1003,11 +1005,11 @@ cudaError_t launch_cross_t(const CUtensorMap& tmap, CrossParams p, int sms, cuda
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  const unsigned pairs = (unsigned)(p.B * ((p.tiles_per_seq + 1) / 2));
-  p.splits = cross_splits((long long)pairs * p.Hkv, p.maxblk, sms);
-  p.by_length = p.B > 1 && p.B <= Gm::kThreads && (long long)pairs * p.Hkv > sms;
+  const unsigned ctas = (unsigned)p.B * (unsigned)((p.tiles_per_seq + 1) / 2) * (unsigned)p.Hkv;
+  p.splits = cross_splits(ctas, p.maxblk, sms);
+  p.by_length = p.B > 1 && p.B <= Gm::kThreads && ctas > (unsigned)sms;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pairs, (unsigned)p.Hkv, (unsigned)p.splits);
+  cfg.gridDim = dim3(ctas, 1, (unsigned)p.splits);
   cfg.blockDim = dim3(Gm::kThreads);
   cfg.dynamicSmemBytes = Gm::kSmem;
   cfg.stream = st;
