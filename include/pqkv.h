@@ -340,7 +340,7 @@ int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_
  * positions [kv_ranges[t][0], kv_ranges[t][1]) cut to [0, kv_lens[b]): the
  * pictures before a token, say. out_row = softmax(scale * q K^T) V over what
  * the token sees; a token that sees nothing (no states, or an empty range) gets
- * a zero row. Keys that a token does not see may hold anything; values among the
+ * a zero row, one that sees a score of NaN a row of NaN. Keys that a token does not see may hold anything; values among the
  * positions [0, kv_lens[b]) must be finite (an unseen one has weight 0, not no
  * weight). Rows of q behind cu_q_lens[batch] are not touched. Other
  * arguments, results and errors as in pqkv_paged_prefill_attention (a

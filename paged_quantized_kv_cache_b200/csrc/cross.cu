@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
       if (dup) st = s_stat[kM + r];
       const float mx = fmaxf(m, st.x);
       const float f = m == -INFINITY ? 0.f : ex2(m - mx), f2 = st.x == -INFINITY ? 0.f : ex2(st.x - mx);
-      const float sum = f * l + f2 * st.y, inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float sum = f * l + f2 * st.y, inv = sum == 0.f ? 0.f : 1.f / sum;  // a sum of NaN stays one
       const float a = f * inv * (Gm::kFp8 ? vref : 1.f), a2 = f2 * inv;
       uint16_t* dst = static_cast<uint16_t*>(p.out) + orow;
 #pragma unroll 1
@@ -950,13 +950,14 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
       float mx = st.x;
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o, 16));
-      // a part without tiles leaves no O and counts nothing
+      // a part without tiles leaves no O and counts nothing (its sum is 0); a
+      // part's sum of NaN makes the row NaN, whatever its max
       float w = st.x == -INFINITY ? 0.f : ex2(st.x - mx);
       float sum = w * st.y;
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o, 16);
       sum = __shfl_sync(kFull, sum, 0, kChunks);
-      w = w > 0.f && sum > 0.f ? w / sum : 0.f;
+      w = sum == 0.f ? 0.f : w / sum;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int k = 0; k < parts; ++k) {

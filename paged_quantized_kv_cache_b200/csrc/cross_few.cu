@@ -32,6 +32,10 @@ namespace {
 
 constexpr int kMaxFewSplits = 16;  // CTAs of a cluster (above 8: opted into)
 
+// What exponents are taken against when the max is m: 0 while nothing has a max,
+// so that 2^(-inf - .) is 0 (-inf - -inf is NaN) and a score of NaN gives NaN.
+__device__ __forceinline__ float finite(float m) { return m == -INFINITY ? 0.f : m; }
+
 template <int KVF, int D, int NT>
 struct FewGeom {
   using Gm = DecodeGeom<KVF, D, NT>;
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[i][nt][e] = mm[nt][e & 1] != kNegInf ? ex2(x[i][nt][e] - mm[nt][e & 1]) : 0.f;
+        for (int e = 0; e < 4; ++e) w[i][nt][e] = ex2(x[i][nt][e] - finite(mm[nt][e & 1]));
 #pragma unroll
       for (int c = 0; c < 2; ++c) ll[nt][c] += (w[0][nt][c] + w[0][nt][c + 2]) + (w[1][nt][c] + w[1][nt][c + 2]);
     }
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
   const float* parts = reinterpret_cast<const float*>(smem);
   constexpr int kStep = Fg::kPart / 4;
   auto store4 = [&](int n, int d, const float4& o, float l) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // a sum of NaN stays one
     const size_t at = row_at(n) + d;
     store_out2<QBF16>(p.out, at, o.x * inv, o.y * inv);
     store_out2<QBF16>(p.out, at + 2, o.z * inv, o.w * inv);
@@ -451,14 +455,12 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < NW; ++k) mx = fmaxf(mx, parts[k * kStep + NC * D + n]);
-    if (mx != kNegInf) {
 #pragma unroll
-      for (int k = 0; k < NW; ++k) {
-        const float f = ex2(parts[k * kStep + NC * D + n] - mx);
-        const float4 a = *reinterpret_cast<const float4*>(parts + k * kStep + n * D + d);
-        l = fmaf(f, parts[k * kStep + NC * D + NC + n], l);
-        o = make_float4(fmaf(f, a.x, o.x), fmaf(f, a.y, o.y), fmaf(f, a.z, o.z), fmaf(f, a.w, o.w));
-      }
+    for (int k = 0; k < NW; ++k) {
+      const float f = ex2(parts[k * kStep + NC * D + n] - finite(mx));
+      const float4 a = *reinterpret_cast<const float4*>(parts + k * kStep + n * D + d);
+      l = fmaf(f, parts[k * kStep + NC * D + NC + n], l);
+      o = make_float4(fmaf(f, a.x, o.x), fmaf(f, a.y, o.y), fmaf(f, a.z, o.z), fmaf(f, a.w, o.w));
     }
     if (S == 1) {
       store4(n, d, o, l);
@@ -478,13 +480,11 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
     float mx = kNegInf, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < S; ++k) mx = fmaxf(mx, ld_peer(at + (uint32_t)(NC * D + n) * 4, k));
-    if (mx != kNegInf) {
-      for (int k = 0; k < S; ++k) {
-        const float f = ex2(ld_peer(at + (uint32_t)(NC * D + n) * 4, k) - mx);
-        const float4 a = ld_peer4(at + (uint32_t)(n * D + d) * 4, k);
-        l = fmaf(f, ld_peer(at + (uint32_t)(NC * D + NC + n) * 4, k), l);
-        o = make_float4(fmaf(f, a.x, o.x), fmaf(f, a.y, o.y), fmaf(f, a.z, o.z), fmaf(f, a.w, o.w));
-      }
+    for (int k = 0; k < S; ++k) {
+      const float f = ex2(ld_peer(at + (uint32_t)(NC * D + n) * 4, k) - finite(mx));
+      const float4 a = ld_peer4(at + (uint32_t)(n * D + d) * 4, k);
+      l = fmaf(f, ld_peer(at + (uint32_t)(NC * D + NC + n) * 4, k), l);
+      o = make_float4(fmaf(f, a.x, o.x), fmaf(f, a.y, o.y), fmaf(f, a.z, o.z), fmaf(f, a.w, o.w));
     }
     store4(n, d, o, l);
   }
