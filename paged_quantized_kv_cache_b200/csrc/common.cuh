@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <cfloat>
 #include <stdint.h>
 
 #include "../../include/pqkv.h"
@@ -58,6 +59,14 @@ __device__ __forceinline__ uint32_t enc_e2m1x2(float lo, float hi) {
   if ((r & 0x7u) == 0) r = (r & 0xF0u) | ((__float_as_uint(lo) >> 28) & 0x8u);
   if ((r & 0x70u) == 0) r = (r & 0x0Fu) | ((__float_as_uint(hi) >> 24) & 0x80u);
   return r;
+}
+
+// e of the power of two 2^-e that a bf16 query row, whose largest |q| is mx, is
+// multiplied by before it is narrowed to f16 (quantized caches): exact, and the
+// largest comes into [2^13, 2^14). Not below -126, so that 2^-e is a float: the
+// largest of a row below 2^-113 stays smaller, at least 2^-7.
+__device__ __forceinline__ int query_exponent(float mx) {
+  return mx > 0.f && mx <= FLT_MAX ? max(ilogbf(mx) - 13, -126) : 0;
 }
 
 // Two FP8 codes (low byte first) -> f16x2 (exact).

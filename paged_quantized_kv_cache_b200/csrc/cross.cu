@@ -50,7 +50,6 @@
 // scores, the V scale P relative to the largest so far (O is kept in units of
 // it). FP4 operands are exact in f16 (E2M1 x E4M3, fp16 outlier values).
 #include <atomic>
-#include <cfloat>
 #include <climits>
 
 #include "attn_math.cuh"
@@ -639,7 +638,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
             mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
         }
       }
-      const int ex = (mx > 0.f && mx <= FLT_MAX) ? ilogbf(mx) - 13 : 0;
+      const int ex = query_exponent(mx);
       qmul = ldexpf(1.f, -ex);
       sl2 = p.scale_log2 * ldexpf(1.f, ex);
     }

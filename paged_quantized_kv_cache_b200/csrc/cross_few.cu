@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
       }
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-      mul = ldexpf(1.f, -((mx > 0.f && mx <= FLT_MAX) ? ilogbf(mx) - 13 : 0));
+      mul = ldexpf(1.f, -query_exponent(mx));
     }
 #pragma unroll
     for (int kk = 0; kk < KT; ++kk) {

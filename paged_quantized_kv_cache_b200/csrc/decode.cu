@@ -505,8 +505,7 @@ __global__ void __launch_bounds__(DecodeGeom<KVF, D, NT>::kWarps * 32, 1)
         }
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-        const int ex = (mx > 0.f && mx <= FLT_MAX) ? ilogbf(mx) - 13 : 0;
-        rowmul[nt] = ldexpf(1.f, -ex);
+        rowmul[nt] = ldexpf(1.f, -query_exponent(mx));
       }
 #pragma unroll
       for (int kk = 0; kk < KT; ++kk) {

@@ -4,8 +4,6 @@
 // (decode.cu) and the cross attention of few tokens (cross_few.cu).
 #pragma once
 
-#include <cfloat>
-
 #include "decode.cuh"
 
 namespace pqkv {

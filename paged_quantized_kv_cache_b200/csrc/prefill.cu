@@ -40,8 +40,6 @@
 // the largest V scale seen so far (O is kept in units of it). FP4 operands are
 // exact in f16 (E2M1 x E4M3 and the fp16 outlier values).
 #include <atomic>
-#include <cfloat>
-
 #include "attn_math.cuh"
 #include "prefill.cuh"
 #include "tcgen05.cuh"
@@ -232,7 +230,7 @@ __global__ void __launch_bounds__(PrefillGeom<KVF, D>::kThreads, 1)
             mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
         }
       }
-      const int ex = (mx > 0.f && mx <= FLT_MAX) ? ilogbf(mx) - 13 : 0;
+      const int ex = query_exponent(mx);
       qmul = ldexpf(1.f, -ex);
       sl2 = p.scale_log2 * ldexpf(1.f, ex);
     }
