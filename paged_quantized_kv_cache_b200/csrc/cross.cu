@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   auto chunk_at = [&](int slot, int c) { return (uint32_t)(slot * kChunks + (c ^ (slot & (kChunks - 1)))) * 16; };
   auto leave_part = [&]() {  // this thread's channels of its row, and m and l
     const int slot = wg * kM + r;
-    if (group == 0) s_stat[slot] = make_float2(m, l);
+    if (group == 0) s_stat[slot] = make_float2(*abort_flag ? NAN : m, l);  // no max is NaN: a part that a wait cut short
     __syncwarp();
     if (tiles_of(wg) > 0) {
       const float vs = Gm::kFp8 ? vref : 1.f;
@@ -946,6 +946,8 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
       const int i = min(i0 + lane / kChunks, n_rows - 1);
       float2 st = make_float2(-INFINITY, 0.f);
       if (c < parts) st = ld_peer2(stat_at + (uint32_t)(i + (c & (par - 1)) * kM) * 8, c >> pshift);
+      // rows of which a part was cut short are left as they are
+      const unsigned cut = __ballot_sync(kFull, isnan(st.x)) & (kChunks == 32 ? kFull : 0xFFFFu << (lane & 16));
       float mx = st.x;
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o, 16));
@@ -966,7 +968,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
         if (f != 0.f)
           acc = make_float4(fmaf(f, o.x, acc.x), fmaf(f, o.y, acc.y), fmaf(f, o.z, acc.z), fmaf(f, o.w, acc.w));
       }
-      if (i0 + lane / kChunks >= n_rows) continue;
+      if (i0 + lane / kChunks >= n_rows || cut) continue;
       uint16_t* dst = static_cast<uint16_t*>(p.out) +
                       ((size_t)(q0 + mt0 * TOK + i / G) * p.Hq + (size_t)h * G + i % G) * D + 4 * c;
       *reinterpret_cast<uint2*>(dst) =

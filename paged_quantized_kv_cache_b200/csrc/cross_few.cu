@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
         part[n * D + dmap<KVF>(mt, g)] = acc[nt][mt][c] * vs;
         part[n * D + dmap<KVF>(mt, g + 8)] = acc[nt][mt][c + 2] * vs;
       }
-      if (g == 0) {
-        part[NC * D + n] = mm[nt][c];
+      if (g == 0) {  // no max is NaN: that marks a part that a wait cut short
+        part[NC * D + n] = aborted ? NAN : mm[nt][c];
         part[NC * D + NC + n] = ll[nt][c];
       }
     }
@@ -453,8 +453,13 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
     const int n = i / (D / 4), d = 4 * (i % (D / 4));
     float mx = kNegInf, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool cut = false;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) mx = fmaxf(mx, parts[k * kStep + NC * D + n]);
+    for (int k = 0; k < NW; ++k) {
+      const float m = parts[k * kStep + NC * D + n];
+      cut |= isnan(m);
+      mx = fmaxf(mx, m);
+    }
 #pragma unroll
     for (int k = 0; k < NW; ++k) {
       const float f = ex2(parts[k * kStep + NC * D + n] - finite(mx));
@@ -463,11 +468,11 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
       o = make_float4(fmaf(f, a.x, o.x), fmaf(f, a.y, o.y), fmaf(f, a.z, o.z), fmaf(f, a.w, o.w));
     }
     if (S == 1) {
-      store4(n, d, o, l);
+      if (!cut) store4(n, d, o, l);
     } else {
       *reinterpret_cast<float4*>(whole + n * D + d) = o;
       if (d == 0) {
-        whole[NC * D + n] = mx;
+        whole[NC * D + n] = cut ? NAN : mx;
         whole[NC * D + NC + n] = l;
       }
     }
@@ -479,7 +484,13 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
     const int n = i / (D / 4), d = 4 * (i % (D / 4));
     float mx = kNegInf, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < S; ++k) mx = fmaxf(mx, ld_peer(at + (uint32_t)(NC * D + n) * 4, k));
+    bool cut = false;
+    for (int k = 0; k < S; ++k) {
+      const float m = ld_peer(at + (uint32_t)(NC * D + n) * 4, k);
+      cut |= isnan(m);
+      mx = fmaxf(mx, m);
+    }
+    if (cut) continue;
     for (int k = 0; k < S; ++k) {
       const float f = ex2(ld_peer(at + (uint32_t)(NC * D + n) * 4, k) - finite(mx));
       const float4 a = ld_peer4(at + (uint32_t)(n * D + d) * 4, k);
