@@ -47,8 +47,7 @@
 // 1700 cycles). Quantized caches: the softmax of 8 warps, 2300 cycles a tile.
 //
 // FP8 scales stay out of the operands: the K scale of a block multiplies its
-// scores, the V scale P relative to the largest so far (O is kept in units of
-// it). FP4 operands are exact in f16 (E2M1 x E4M3, fp16 outlier values).
+// scores, the V scale P (move_unit). FP4 operands are exact in f16 (E2M1 x E4M3, fp16 outlier values).
 #include <atomic>
 #include <climits>
 
@@ -176,10 +175,12 @@ __device__ __forceinline__ float exponents(uint32_t t_s, float nm, const float (
   return (ra[0] + ra[1]) + (rb[0] + rb[1]);
 }
 
-// The largest of a row's scores x cj (kMasked: of those in `cols`).
-template <bool kMasked>
-__device__ __forceinline__ float largest(uint32_t t_s, const float (&cj)[4], uint64_t cols) {
-  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+// The largest of a row's scores x cj (kMasked: of those in `cols`); kPerBlock:
+// mx[j] is that of block j.
+template <bool kMasked, bool kPerBlock>
+__device__ __forceinline__ float largest(uint32_t t_s, const float (&cj)[4], uint64_t cols, float (&mx)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) mx[j] = -INFINITY;
   uint32_t x[2][16];
   tc::tmem_ld16_start(t_s, x[0]);
 #pragma unroll
@@ -189,7 +190,10 @@ __device__ __forceinline__ float largest(uint32_t t_s, const float (&cj)[4], uin
     if (j < 3) tc::tmem_ld16_start(t_s + 16 * (j + 1), x[(j + 1) & 1]);
 #pragma unroll
     for (int c = 0; c < 16; ++c)
-      if (!kMasked || ((cols >> (16 * j + c)) & 1)) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[j & 1][c]) * cj[j]);
+      if (!kMasked || ((cols >> (16 * j + c)) & 1)) {
+        float& most = mx[kPerBlock ? j : c & 3];
+        most = fmaxf(most, __uint_as_float(x[j & 1][c]) * cj[j]);
+      }
   }
   return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  float m = -INFINITY, l = 0.f, vref = 0.f;  // this row's max, sum (of this thread's tiles), FP8 unit of O
+  float m = -INFINITY, l = 0.f, unit = 0.f;  // this row's max, sum (of this thread's tiles), FP8: 1 / unit of O
   bool aborted = false;
 
   if (warp >= Gm::kProducer && warp < Gm::kMma) {
@@ -671,7 +675,6 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     // a warp without rows has only zeros to leave in the Q tile
     const int w0 = dup ? wg : 0, U = quad < warps_of(wg) ? tiles_of(wg) : 0;
     bool ok = true;      // no wait of this thread has timed out
-    float rvref = 0.f;   // FP8: 1 / vref (0 while vref is 0)
     int moves = 0;       // H = 2: moves of the max that this warp has followed
     // tiles [whole_lo, whole_hi) of the CTA lie inside this row's range, tiles
     // below none_hi and from none_lo on outside it; those below t_full end
@@ -709,7 +712,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
         cj[j] = none ? 0.f : sl2;
         vr[j] = 1.f;
       }
-      float top = vref;  // FP8: the largest V scale so far, this tile's included (the same on every thread)
+      float most_v = 1.f;  // FP8: the largest factor of P, or 1
       if constexpr (Gm::kFp8) {
         const float4 k4 = *reinterpret_cast<const float4*>(tile_sk + (t % Gm::kScaleSlots) * 4);
         const float4 v4 = *reinterpret_cast<const float4*>(tile_sv + (t % Gm::kScaleSlots) * 4);
@@ -717,20 +720,17 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           cj[j] *= k[j];
-          vr[j] = v[j];
-          top = fmaxf(top, v[j]);  // a block without data has scale 0
+          vr[j] = none ? 0.f : v[j] * unit;  // a block without data has scale 0
+          most_v = fmaxf(most_v, vr[j]);
         }
-        if (top > vref) rvref = 1.f / top;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) vr[j] *= rvref;  // <= 1 up to an ulp
       }
       uint32_t pk[32];
       float sum = 0.f;
       // the usual way, against the max as this warp knows it
       auto usual = [&]() -> bool {
-        if (!__all_sync(kFull, plain && top == vref && (none || m != -INFINITY))) return false;
+        if (!__all_sync(kFull, plain && (none || m != -INFINITY))) return false;
         sum = exponents<false, Gm::kFp8, kBfMma>(t_s, none ? -INFINITY : -m, cj, vr, 0, pk);
-        return __all_sync(kFull, sum <= kMost);
+        return __all_sync(kFull, sum * most_v <= kMost);
       };
       bool done = usual();
       if constexpr (H == 2) {
@@ -780,16 +780,26 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
         // a row that sees nothing of a plain tile goes by its mask: 0 x a key's NaN
         // or infinity is what brought it here
         const bool whole = __all_sync(kFull, plain && !none);
-        const float mx = whole ? largest<false>(t_s, cj, 0) : largest<true>(t_s, cj, cols);
+        float mb[4];
+        const float mx = whole ? largest<false, Gm::kFp8>(t_s, cj, 0, mb) : largest<true, Gm::kFp8>(t_s, cj, cols, mb);
         float fo = 1.f;  // rescale of l and O for a larger row max
         if (mx > m + kLazy && !none) {
           fo = ex2(m - mx);  // 0 when m was -inf
           m = mx;
         }
         l *= fo;
-        if (Gm::kFp8 && top > vref) {  // O moves to units of a larger V scale
-          fo *= vref / top;
-          vref = top;
+        if constexpr (Gm::kFp8) {
+          const float4 v4 = *reinterpret_cast<const float4*>(tile_sv + (t % Gm::kScaleSlots) * 4);
+          const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+          float need = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            vr[j] = ((cols >> (16 * j)) & 0xFFFF) ? v[j] : 0.f;  // blocks that the row sees
+            need = fmaxf(need, ex2(mb[j] - (m == -INFINITY ? 0.f : m)) * vr[j]);
+          }
+          fo = move_unit(unit, fo, need, m != -INFINITY);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) vr[j] = fminf(vr[j] * unit, FLT_MAX);  // finite where every p is 0
         }
         __syncwarp();
         if (whole)
@@ -874,7 +884,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
     if (group == 0) s_stat[slot] = make_float2(*abort_flag ? NAN : m, l);  // no max is NaN: a part that a wait cut short
     __syncwarp();
     if (tiles_of(wg) > 0) {
-      const float vs = Gm::kFp8 ? vref : 1.f;
+      const float vs = Gm::kFp8 ? (unit > 0.f ? 1.f / unit : 0.f) : 1.f;
 #pragma unroll 1
       for (int c0 = group * (D / H); c0 < (group + 1) * (D / H); c0 += 32) {
         uint32_t o[32];
@@ -898,7 +908,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
       const float mx = fmaxf(m, st.x);
       const float f = m == -INFINITY ? 0.f : ex2(m - mx), f2 = st.x == -INFINITY ? 0.f : ex2(st.x - mx);
       const float sum = f * l + f2 * st.y, inv = sum == 0.f ? 0.f : 1.f / sum;  // a sum of NaN stays one
-      const float a = f * inv * (Gm::kFp8 ? vref : 1.f), a2 = f2 * inv;
+      const float a = f * inv * (Gm::kFp8 ? (unit > 0.f ? 1.f / unit : 0.f) : 1.f), a2 = f2 * inv;
       uint16_t* dst = static_cast<uint16_t*>(p.out) + orow;
 #pragma unroll 1
       for (int c0 = group * (D / H); c0 < (group + 1) * (D / H); c0 += 32) {

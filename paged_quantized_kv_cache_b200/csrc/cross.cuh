@@ -60,6 +60,28 @@ __device__ __forceinline__ int nth_longest(const int32_t* kv_lens, int B, int b,
   return chosen;
 }
 
+// FP8 states: O of a row is kept in units of 1 / r, and P enters its product
+// with V, in f16, as p s r (s: the V scale of a key's block). The unit goes by
+// the largest p s of what the row itself has seen: the scales alone, or those of
+// all blocks read, would leave a row of small values beside large ones without
+// bits. After a step that moved the row's max (l was multiplied by fl; `any`: the
+// row has a max) and brought p s up to `need`: the new r, and what O is
+// multiplied by. The unit rises when p s r would pass 2^8, and falls with l, as
+// long as r is a float; r is 0 while the row has no max.
+__device__ __forceinline__ float move_unit(float& r, float fl, float need, bool any) {
+  constexpr float kMost = 0x1p126f;
+  const float was = r;
+  if (was == 0.f) {
+    r = any ? fminf(1.f / need, kMost) : 0.f;
+    return fl;
+  }
+  const bool rises = need * was > 256.f * fl;
+  const float to = rises ? 1.f / need : was / fl;
+  r = fminf(to, kMost);
+  if (!rises && r == to) return 1.f;
+  return fl > 0.f ? fl * (r / was) : 0.f;
+}
+
 // Tiles of 128 query rows on tcgen05 (cross.cu; the prefill's tensor map for
 // 16-bit caches), or at most kFewColumns rows per KV head (cross_few.cu; the
 // decode's tensor map).

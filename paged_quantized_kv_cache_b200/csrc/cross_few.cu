@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
 
   // ---- online softmax over this warp's blocks, two at a time ----
   float acc[NT][KT][4] = {};
-  float mm[NT][2], ll[NT][2], vref = 0.f, rvref = 0.f;
+  float mm[NT][2], ll[NT][2];
+  float unit[NT][2] = {}, units = 0.f;  // FP8: 1 / unit of O of the lane's columns (move_unit), and the largest
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     mm[nt][0] = mm[nt][1] = kNegInf;
@@ -306,8 +307,9 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
     float fc[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) fc[nt][0] = fc[nt][1] = 1.f;
-    bool rescale = __any_sync(kFull, grows);
-    if (rescale) {
+    // FP8: p is at most 2^8 (kLazy), so p s r stays below 2^15 unless
+    if constexpr (Gm::kFp8) grows |= fmaxf(use[0] ? sv[0] : 0.f, use[1] ? sv[1] : 0.f) * units > 128.f;
+    if (__any_sync(kFull, grows)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -318,26 +320,24 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
           }
           ll[nt][c] *= fc[nt][c];
         }
-    }
-    // FP8 V scales: O is kept in units of the largest so far; others enter through P
-    float pr[2] = {1.f, 1.f};
-    if constexpr (Gm::kFp8) {
-      const float top = fmaxf(use[0] ? sv[0] : 0.f, use[1] ? sv[1] : 0.f);
-      if (top > vref) {
-        const float r = vref / top;
+      if constexpr (Gm::kFp8) {
+        units = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          fc[nt][0] *= r;
-          fc[nt][1] *= r;
-        }
-        vref = top;
-        rvref = 1.f / top;
-        rescale = true;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float need = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float mb = fmaxf(x[i][nt][c], x[i][nt][c + 2]);  // the max of block i alone
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, o));
+              if (mb != kNegInf) need = fmaxf(need, ex2(mb - finite(mm[nt][c])) * sv[i]);
+            }
+            fc[nt][c] = move_unit(unit[nt][c], fc[nt][c], need, mm[nt][c] != kNegInf);
+            if (8 * nt + 2 * qd + c < nc) units = fmaxf(units, unit[nt][c]);
+          }
       }
-      pr[0] = use[0] ? sv[0] * rvref : 0.f;
-      pr[1] = use[1] ? sv[1] * rvref : 0.f;
-    }
-    if (rescale) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -375,12 +375,17 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
     // token each, 144 against 136 us.
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (!use[i] || (Gm::kFp8 && !(pr[i] > 0.f))) continue;
+      if (!use[i] || (Gm::kFp8 && sv[i] == 0.f)) continue;
       uint32_t b0[NT], b1[NT], c0[NT], c1[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float w0 = w[i][nt][0] * pr[i], w1 = w[i][nt][1] * pr[i];
-        const float w2 = w[i][nt][2] * pr[i], w3 = w[i][nt][3] * pr[i];
+        float pr[2] = {1.f, 1.f};
+        if constexpr (Gm::kFp8) {
+          pr[0] = fminf(sv[i] * unit[nt][0], FLT_MAX);  // finite where every p is 0
+          pr[1] = fminf(sv[i] * unit[nt][1], FLT_MAX);
+        }
+        const float w0 = w[i][nt][0] * pr[0], w1 = w[i][nt][1] * pr[1];
+        const float w2 = w[i][nt][2] * pr[0], w3 = w[i][nt][3] * pr[1];
         const uint32_t hA = pack_f32x2(w0, w1, kBf16Mma), hB = pack_f32x2(w2, w3, kBf16Mma);
         b0[nt] = movmatrix_t(hA);
         b1[nt] = movmatrix_t(hB);
@@ -423,12 +428,12 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
   }
   __syncthreads();  // every warp is done with its tiles
   float* part = reinterpret_cast<float*>(smem + warp * Fg::kPart);  // O [NC][D], m [NC], l [NC]
-  const float vs = Gm::kFp8 ? vref : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int n = 8 * nt + 2 * qd + c;
+      const float vs = Gm::kFp8 ? (unit[nt][c] > 0.f ? 1.f / unit[nt][c] : 0.f) : 1.f;
 #pragma unroll
       for (int mt = 0; mt < KT; ++mt) {
         part[n * D + dmap<KVF>(mt, g)] = acc[nt][mt][c] * vs;
