@@ -54,7 +54,6 @@
 #include "attn_math.cuh"
 #include "cluster.cuh"
 #include "cross.cuh"
-#include "tcgen05.cuh"
 
 namespace pqkv {
 

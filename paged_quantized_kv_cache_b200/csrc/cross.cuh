@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "tcgen05.cuh"
 
 namespace pqkv {
 
@@ -56,6 +57,7 @@ __device__ __forceinline__ int nth_longest(const int32_t* kv_lens, int B, int b,
   }
   __syncthreads();
   const int chosen = scratch[B];
+  tc::fence_smem_to_async();  // the next to write the scratch may be a TMA copy
   __syncthreads();
   return chosen;
 }

@@ -76,7 +76,8 @@ __device__ __forceinline__ void fence_before_sync() {
 __device__ __forceinline__ void fence_after_sync() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// Generic-proxy shared-memory writes become visible to the tensor cores.
+// Generic-proxy shared-memory accesses come before what the async proxy (tensor
+// cores, TMA) does behind the next barrier.
 __device__ __forceinline__ void fence_smem_to_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
