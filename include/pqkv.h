@@ -340,15 +340,17 @@ int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_
  * positions [kv_ranges[t][0], kv_ranges[t][1]) cut to [0, kv_lens[b]): the
  * pictures before a token, say. out_row = softmax(scale * q K^T) V over what
  * the token sees; a token that sees nothing (no states, or an empty range) gets
- * a zero row, one that sees a score of NaN a row of NaN. Keys that a token does not see may hold anything; values among the
- * positions [0, kv_lens[b]) must be finite (an unseen one has weight 0, not no
- * weight). Rows of q behind cu_q_lens[batch] are not touched. Other
+ * a zero row, one that sees a score of NaN a row of NaN. Keys that a token does
+ * not see may hold anything; values among the positions [0, kv_lens[b]) must be
+ * finite (an unseen one has weight 0, not no weight), bf16 ones below 2^70 in
+ * magnitude. Rows of q behind cu_q_lens[batch] are not touched. Other
  * arguments, results and errors as in pqkv_paged_prefill_attention (a
  * kv_lens[b] below 0 or above 16 * max_blocks_per_seq gives zero rows and
  * PQKV_DEVERR_SEQ_LEN). P is rounded to 16 bits for its product with V (fp32
  * sums). max_q_len chooses between two kernels: up to 16 query rows (tokens x
  * heads) per KV head the decode's way with a block, above that tcgen05 tiles of
- * 128 rows. One kernel on `stream`; no workspace. batch = 0 does nothing. With one token in each of `batch` sequences and no ranges
+ * 128 rows. One kernel on `stream`; no workspace. batch = 0 does nothing. With
+ * one token in each of `batch` sequences and no ranges
  * pqkv_paged_decode_attention computes the same.
  */
 int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_len, int num_q_heads,

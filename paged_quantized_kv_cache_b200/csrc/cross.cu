@@ -27,7 +27,7 @@
 // has a max from earlier tiles. That max then stays: exponents are taken against
 // it while the scores arrive, 16 columns (a cache block) at a time, without a
 // max of the tile, and only a row sum that shows a much larger score (f16 P:
-// 2^15, bf16 P, which has the range of fp32: 2^60) takes the tile again the
+// 2^15, bf16 P: 2^30) takes the tile again the
 // general way: masks, max, rescaling of O and l. With H = 2 the warps of a row's
 // two groups hand P over in the order of the tiles (a turn per 32 rows): the
 // max is shared, and a warp whose turn comes after the max was moved takes its
@@ -686,7 +686,9 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
       none_hi = my_lo / kN - t0;
       none_lo = (my_hi + kN - 1) / kN - t0;
     }
-    constexpr float kMost = kBfMma ? 0x1p60f : 0x1p15f;  // largest row sum of a tile: P fits its type
+    // largest row sum of a tile: f16 P fits its type; bf16 P leaves values below
+    // 2^70 room in the sums over 2^25 tiles
+    constexpr float kMost = kBfMma ? 0x1p30f : 0x1p15f;
     // the max was moved by the row's other group: l follows
     auto follow = [&]() {
       const float to = row_max[wg * kM + r];
