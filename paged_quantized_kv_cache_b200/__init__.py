@@ -131,7 +131,8 @@ def _load_binding():
         raise ImportError("_binding.so is missing or does not load (run: python -m paged_quantized_kv_cache_b200.build): "
                           "%s" % e) from e
     module.bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
-        "pqkv_build_batch", "pqkv_qk_norm_rope", "pqkv_qkv_norm_rope_write", "pqkv_paged_cross_attention")))
+        "pqkv_build_batch", "pqkv_qk_norm_rope", "pqkv_qkv_norm_rope_write", "pqkv_paged_cross_attention",
+        "pqkv_cache_layout")))
     _binding_module = module
     return module
 

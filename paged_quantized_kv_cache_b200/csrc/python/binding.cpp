@@ -23,6 +23,7 @@ decltype(&pqkv_build_batch) f_build_batch = nullptr;
 decltype(&pqkv_qk_norm_rope) f_qk_norm_rope = nullptr;
 decltype(&pqkv_qkv_norm_rope_write) f_qkv_norm_rope_write = nullptr;
 decltype(&pqkv_paged_cross_attention) f_paged_cross_attention = nullptr;
+decltype(&pqkv_cache_layout) f_cache_layout = nullptr;
 
 struct Refused {
   std::string why;
@@ -147,14 +148,15 @@ int launch(F f, A... a) {
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> int {
-    need(n == 4, "expected four addresses");
-    void* f[4];
-    for (int i = 0; i < 4; ++i) f[i] = PyLong_AsVoidPtr(a[i]);
+    need(n == 5, "expected five addresses");
+    void* f[5];
+    for (int i = 0; i < 5; ++i) f[i] = PyLong_AsVoidPtr(a[i]);
     need(!PyErr_Occurred(), "addresses must be integers");
     f_build_batch = reinterpret_cast<decltype(f_build_batch)>(f[0]);
     f_qk_norm_rope = reinterpret_cast<decltype(f_qk_norm_rope)>(f[1]);
     f_qkv_norm_rope_write = reinterpret_cast<decltype(f_qkv_norm_rope_write)>(f[2]);
     f_paged_cross_attention = reinterpret_cast<decltype(f_paged_cross_attention)>(f[3]);
+    f_cache_layout = reinterpret_cast<decltype(f_cache_layout)>(f[4]);
     return PQKV_OK;
   });
 }
@@ -279,23 +281,32 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // cache, scales, outliers_idx, outliers_val (None where a format has none),
-// kv_dtype, num_blocks, num_kv_heads, head_dim
+// kv_dtype, num_blocks, num_kv_heads, head_dim: the kernels go by these numbers,
+// so each array must hold what they make of it
 struct CacheArgs {
   void* arrays[4] = {nullptr, nullptr, nullptr, nullptr};
   int kv_dtype, num_blocks, heads, D;
   explicit CacheArgs(Args& x) {
     const char* names[4] = {"cache", "scales", "outliers_idx", "outliers_val"};
+    const at::Tensor* given[4] = {nullptr, nullptr, nullptr, nullptr};
     for (int i = 0; i < 4; ++i) {
-      if (x.none()) {
-        x.skip();
-        continue;
-      }
-      arrays[i] = x.tensor(names[i], at::kByte).data_ptr();
+      if (x.none()) x.skip();
+      else given[i] = &x.tensor(names[i], at::kByte);
     }
     kv_dtype = x.small("kv_dtype");
     num_blocks = x.small("num_blocks");
     heads = x.small("num_kv_heads");
     D = x.small("head_dim");
+    need(f_cache_layout != nullptr, "the library is not bound");
+    size_t bytes[4] = {0, 0, 0, 0};
+    f_cache_layout(kv_dtype, num_blocks, heads, D, bytes);  // numbers that it refuses, the call itself refuses
+    for (int i = 0; i < 4; ++i) {
+      if (!given[i]) continue;
+      if ((size_t)given[i]->numel() < bytes[i])
+        throw Refused{std::string(names[i]) + " must have at least " + std::to_string(bytes[i]) +
+                      " bytes for this num_blocks, num_kv_heads and head_dim"};
+      arrays[i] = given[i]->data_ptr();
+    }
   }
 };
 
