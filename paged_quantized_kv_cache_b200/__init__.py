@@ -130,6 +130,10 @@ def _load_binding():
     except ImportError as e:
         raise ImportError("_binding.so is missing or does not load (run: python -m paged_quantized_kv_cache_b200.build): "
                           "%s" % e) from e
+    from .build import binding_target
+    if getattr(module, "BUILT_FOR", None) != binding_target():
+        raise ImportError("_binding.so was built %s, not %s (run: python -m paged_quantized_kv_cache_b200.build)"
+                          % (getattr(module, "BUILT_FOR", "for another torch"), binding_target()))
     module.bind(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in (
         "pqkv_build_batch", "pqkv_qk_norm_rope", "pqkv_qkv_norm_rope_write", "pqkv_paged_cross_attention",
         "pqkv_cache_layout")))

@@ -51,6 +51,20 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_target() -> str:
+    """What a build of the Python module is good for: the running Python and torch, whose headers it is compiled
+    against. The module holds this as BUILT_FOR."""
+    import torch
+    return "for python %d.%d, torch %s" % (*sys.version_info[:2], torch.__version__)
+
+
+def _binding_stale() -> bool:
+    if _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pqkv.h"), __file__]):
+        return True
+    with open(BINDING, "rb") as f:
+        return binding_target().encode() + b"\0" not in f.read()
+
+
 def _binding_command(out: str):
     """Host compile of the Python module against the headers and libraries of the running Python and torch (which
     its process has loaded before it)."""
@@ -61,6 +75,7 @@ def _binding_command(out: str):
                os.path.join(ROOT, "include")]
     abi = "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch.compiled_with_cxx11_abi())
     return [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", abi,
+            "-DPQKV_BUILT_FOR=\"%s\"" % binding_target(),
             *("-isystem" + i for i in include), BINDING_SRC, "-o", out, *libs]
 
 
@@ -81,7 +96,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             jobs.append([nvcc] + flags + ["-c", src, "-o", obj])
 
     binding_tmp = BINDING + ".tmp%d" % os.getpid()
-    make_binding = force or _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pqkv.h"), __file__])
+    make_binding = force or _binding_stale()
     if make_binding:
         jobs.append(_binding_command(binding_tmp))
 
@@ -95,9 +110,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
-                failed.append(cmd[-3])
+                failed.append(next(a for a in cmd if a.startswith(CSRC)))
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
+        raise RuntimeError("compilation failed for: " + ", ".join(failed))
     if make_binding:
         os.replace(binding_tmp, BINDING)
     if force or _stale(LIB, objs):
