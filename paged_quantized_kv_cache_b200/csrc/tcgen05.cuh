@@ -1,5 +1,5 @@
 // tcgen05.cuh -- thin wrappers of the sm_100a tensor-core (tcgen05) and tensor
-// memory instructions used by the prefill kernel.
+// memory instructions used by the prefill and cross attention kernels.
 //
 // Operand tiles in shared memory use the 128-byte swizzle: rows of 128 bytes,
 // 8-row atoms of 1024 bytes (1024-byte aligned), the 16-byte chunk c of row r
@@ -130,16 +130,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                :
                : "memory");
-}
-
-// Store 16 columns of this thread's lane and wait until they are written.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
-      "tcgen05.wait::st.sync.aligned;"
-      :
-      : "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
 }
 
 // 64 consecutive 32-bit columns of this thread's lane in one load, waited for
