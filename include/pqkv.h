@@ -452,8 +452,8 @@ int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch
  * ([num_heads][head_dim]), q_stride / k_stride elements from one token to the
  * next (multiples of 8, at least one token's heads): parts of a fused
  * projection's output. q_out, k_out: [num_tokens][heads][head_dim] contiguous;
- * either may be its input if that is contiguous too, other overlaps are
- * PQKV_ERR_ARG. num_kv_heads = 0: queries only (k and k_out unused).
+ * either may be its input if that is contiguous too, other overlaps (with any
+ * array of the call) are PQKV_ERR_ARG. num_kv_heads = 0: queries only (k and k_out unused).
  * positions: device int32 [num_axes][num_tokens], 1 <= num_axes <= 4.
  * axis_of_pair: host bytes [rot_dim / 2] below num_axes, or NULL (all axis 0).
  * cos_sin: device float [num_positions][rot_dim], cosines then sines of a

@@ -5,6 +5,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "batch.cuh"
@@ -187,6 +188,24 @@ bool out_ok(const Heads& out, const Heads* in, int n_in, int own, int T, int D) 
     if (i != own || out.p != in[i].p || (T > 1 && in[i].stride != out.stride)) return false;
   }
   return true;
+}
+
+// An output shares no memory with what the call reads beside its rows, or with
+// what else it writes.
+struct Bytes {
+  const void* p;
+  size_t n;
+};
+bool clear_of(const Heads& out, int T, int D, std::initializer_list<Bytes> others) {
+  for (const Bytes& x : others)
+    if (x.p && x.n && overlap(out.p, out.bytes(T, D), x.p, x.n)) return false;
+  return true;
+}
+bool clear_of_params(const Heads& out, const RowParams& r, int T, int D, const int32_t* err) {
+  const size_t row = (size_t)D * sizeof(float);
+  return clear_of(out, T, D,
+                  {{r.q_weight, row}, {r.k_weight, row}, {r.rot ? r.positions : nullptr, (size_t)r.axes * T * 4},
+                   {r.rot ? r.cos_sin : nullptr, (size_t)r.num_pos * r.rot * 4}, {err, 4}});
 }
 
 // The rotary kernel's grid: a row of CTAs for each chunk of at least 8 heads.
@@ -681,6 +700,8 @@ int pqkv_qk_norm_rope(const void* q, const void* k, int dtype, int num_tokens, i
   if (num_kv_heads &&
       (!heads_ok(in[1], D) || !heads_ok(ko, D) || !out_ok(ko, in, 2, 1, T, D) || !out_ok(qo, &ko, 1, -1, T, D)))
     return PQKV_ERR_ARG;
+  if (!clear_of_params(qo, p.r, T, D, err_flag) || (num_kv_heads && !clear_of_params(ko, p.r, T, D, err_flag)))
+    return PQKV_ERR_ARG;
   p.q = q;
   p.k = k;
   p.qs = q_stride;
@@ -720,7 +741,14 @@ int pqkv_qkv_norm_rope_write(const void* q, const void* k, const void* v, int dt
   const Heads in[3] = {{q, num_q_heads, q_stride}, {k, num_kv_heads, k_stride}, {v, num_kv_heads, v_stride}};
   const Heads qo{q_out, num_q_heads, (int64_t)num_q_heads * D};
   if (!err_flag || !slot_mapping || !cache || !aligned16(cache) || !heads_ok(in[0], D) || !heads_ok(in[1], D) ||
-      !heads_ok(in[2], D) || !heads_ok(qo, D) || !out_ok(qo, in, 3, 0, T, D))
+      !heads_ok(in[2], D) || !heads_ok(qo, D) || !out_ok(qo, in, 3, 0, T, D) ||
+      !clear_of_params(qo, p.r, T, D, err_flag))
+    return PQKV_ERR_ARG;
+  size_t bytes[4];
+  if (pqkv_cache_layout(kv_dtype, num_blocks, num_kv_heads, D, bytes) != PQKV_OK ||
+      !clear_of(qo, T, D,
+                {{slot_mapping, (size_t)T * 4}, {cache, bytes[0]}, {scales, bytes[1]}, {outliers_idx, bytes[2]},
+                 {outliers_val, bytes[3]}}))
     return PQKV_ERR_ARG;
   if (!is_16(kv_dtype) && (!scales || !aligned16(scales))) return PQKV_ERR_ARG;
   if (kv_dtype == PQKV_DTYPE_FP4_E2M1 &&
