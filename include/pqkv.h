@@ -346,10 +346,14 @@ int pqkv_paged_prefill_attention(const void* q, int q_dtype, int batch, int max_
  * magnitude. Rows of q behind cu_q_lens[batch] are not touched. Other
  * arguments, results and errors as in pqkv_paged_prefill_attention (a
  * kv_lens[b] below 0 or above 16 * max_blocks_per_seq gives zero rows and
- * PQKV_DEVERR_SEQ_LEN). P is rounded to 16 bits for its product with V (fp32
- * sums). max_q_len chooses between two kernels: up to 16 query rows (tokens x
- * heads) per KV head the decode's way with a block, above that tcgen05 tiles of
- * 128 rows. One kernel on `stream`; no workspace. batch = 0 does nothing. With
+ * PQKV_DEVERR_SEQ_LEN). max_blocks_per_seq is at most 2^27 - 9. P is rounded to
+ * 16 bits for its product with V (fp32 sums). max_q_len chooses between two
+ * kernels: up to 16 query rows (tokens x heads) per KV head the decode's way
+ * with a block, above that tcgen05 tiles of 128 rows, where the rows of the last
+ * tile that max_q_len reaches are computed and rows past it set
+ * PQKV_DEVERR_SEQ_LEN. The states are split between CTAs by the width of the
+ * block tables: a table much wider than its longest sequence leaves some of them
+ * without work. One kernel on `stream`; no workspace. batch = 0 does nothing. With
  * one token in each of `batch` sequences and no ranges
  * pqkv_paged_decode_attention computes the same.
  */

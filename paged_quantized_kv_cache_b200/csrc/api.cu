@@ -577,8 +577,9 @@ int pqkv_paged_cross_attention(const void* q, int q_dtype, int batch, int max_q_
                                int32_t* err_flag, pqkv_stream_t stream) {
   if (!is_kv_dtype(kv_dtype) || (q_dtype != PQKV_DTYPE_FP16 && q_dtype != PQKV_DTYPE_BF16)) return PQKV_ERR_ARG;
   if (is_16(kv_dtype) && q_dtype != kv_dtype) return PQKV_ERR_ARG;
+  // positions, rounded up to two KV tiles, fit 32 bits
   if (batch < 0 || max_q_len < 1 || num_q_heads < 1 || num_kv_heads < 1 || num_blocks < 1 ||
-      max_blocks_per_seq < 1 || max_blocks_per_seq > INT32_MAX / PQKV_BLOCK_SIZE ||
+      max_blocks_per_seq < 1 || max_blocks_per_seq > INT32_MAX / PQKV_BLOCK_SIZE - 8 ||
       (head_dim != 64 && head_dim != 128))
     return PQKV_ERR_ARG;
   if (num_q_heads % num_kv_heads != 0) return PQKV_ERR_ARG;

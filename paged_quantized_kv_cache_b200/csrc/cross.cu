@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(CrossGeom<KVF, D>::kThreads, 1)
   if (p.by_length) b = nth_longest(p.kv_lens, p.B, b, reinterpret_cast<int*>(smem));
   const int q0 = p.cu_q[b], qn = p.cu_q[b + 1] - q0;
   const int L = p.kv_lens[b];
-  if (mt0 == 0 && h == 0 && rank == 0 && tid == 0 && qn > p.tiles_per_seq * TOK)
+  if (mt0 == 0 && h == 0 && rank == 0 && tid == 0 && qn > (long long)p.tiles_per_seq * TOK)
     raise_flag(p.err, PQKV_DEVERR_SEQ_LEN);  // rows past max_q_len are not computed
   if (qn <= 0 || mt0 * TOK >= qn) return;
   const bool rejected = L < 0 || L > kBlock * p.maxblk;
