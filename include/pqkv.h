@@ -430,9 +430,9 @@ int pqkv_swap_in(void* cache, void* scales, void* outliers_idx, void* outliers_v
  * no blocks and seq_lens 0. An id outside [0, num_blocks), in new_block_ids or
  * in the table entry of a request's open block, sets PQKV_DEVERR_BLOCK_ID; its
  * tokens get slot -1 and a new one's table entry is -1. A table row belongs to
- * one request. An output that overlaps another array -> PQKV_ERR_ARG. batch <= PQKV_MAX_BATCH; with batch =
- * 0 only the padding and cu_q_lens[0] are written. One kernel
- * on `stream`; no workspace.
+ * one request. An output that overlaps another array -> PQKV_ERR_ARG.
+ * batch <= PQKV_MAX_BATCH; with batch = 0 only the padding and cu_q_lens[0] are
+ * written. One kernel on `stream`; no workspace.
  */
 int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch,
                      const int32_t* new_block_ids, int num_new_blocks, int32_t* block_tables,
@@ -445,7 +445,7 @@ int pqkv_build_batch(const int32_t* start_pos, const int32_t* num_new, int batch
  * the projection's output, which precedes the cache write and the attention (the
  * pages take K and V as given). Row x (one head of one token, head_dim
  * channels): y = x / sqrt(mean(x^2) + eps) * weight, in fp32 (finite rows of
- * |x| < 2^60), with q_weight or k_weight (device float [head_dim]; NULL = no
+ * |x| < 2^60, and where eps is 0 one channel at least of 2^-60), with q_weight or k_weight (device float [head_dim]; NULL = no
  * norm of those rows). Then, with r = rot_dim / 2, pair i < r of the first
  * rot_dim channels turns by the token's position on the pair's axis:
  *   p = positions[axis_of_pair[i]][token], c = cos_sin[p][i], s = cos_sin[p][r + i]
@@ -482,7 +482,8 @@ int pqkv_qk_norm_rope(const void* q, const void* k, int dtype, int num_tokens, i
  * results are the same, bit for bit. v: as k, v_stride elements from one token
  * to the next. num_kv_heads >= 1; other arguments, rules on runs and errors as
  * in the two calls (a token whose position lies outside the table has a zero
- * key). 16-bit caches: one kernel; FP8 and FP4: two.
+ * key). 16-bit caches: one kernel; FP8 and FP4: two, which take no copies of keys
+ * and values but up to 1.6 times as long as the two calls.
  */
 int pqkv_qkv_norm_rope_write(const void* q, const void* k, const void* v, int dtype, int num_tokens,
                              int num_q_heads, int num_kv_heads, int head_dim, int64_t q_stride,

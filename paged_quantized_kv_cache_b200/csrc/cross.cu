@@ -38,16 +38,18 @@
 // as in the prefill would be half as many products again.
 //
 // Measured (16 sequences of 300-512 tokens over 3203-6404 bf16 states, 32 / 8
-// heads of 128): 547 us, 936 TFLOP/s, when every token sees all states; 527-565 us
+// heads of 128): 537 us, 953 TFLOP/s, when every token sees all states; 507-561 us
 // with ranges that leave 37% of them visible (a CTA walks the tiles from the
-// first to the last position that any of its rows sees). 8 sequences of 129-512 tokens over 1000-4096
-// FP4 states: 172 us, 624 TFLOP/s (190 us with the heads as the grid's slow
-// axis, where the last head's longest sequences start late). With 16-bit caches the tensor pipe bounds it: S of 64
+// first to the last position that any of its rows sees). FP8 states: 566 us, 904
+// TFLOP/s, and 589 with ranges. 8 sequences of 129-512 tokens over 1000-4096 FP4
+// states: 173 us, 620 TFLOP/s (190 us with the heads as the grid's slow axis,
+// where the last head's longest sequences start late). With 16-bit caches the tensor pipe bounds it: S of 64
 // columns reads shared memory for most of a tile pair's time (about 1376 of
 // 1700 cycles). Quantized caches: the softmax of 8 warps, 2300 cycles a tile.
 //
 // FP8 scales stay out of the operands: the K scale of a block multiplies its
-// scores, the V scale P (move_unit). FP4 operands are exact in f16 (E2M1 x E4M3, fp16 outlier values).
+// scores, the V scale P (move_unit). FP4 operands are exact in f16 (E2M1 x E4M3,
+// fp16 outlier values).
 #include <atomic>
 #include <climits>
 

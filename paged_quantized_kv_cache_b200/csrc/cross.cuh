@@ -10,11 +10,12 @@ namespace pqkv {
 
 // Query rows (tokens x query heads) per KV head up to which the few-rows kernel
 // runs. It against the many-rows kernel, 16 sequences of 1400-1500 states, 32 / 8
-// heads of 128, us: 4 rows bf16 21.2 / 25.1, FP8 18.8 / 35.6, FP4 23.0 / 40.4;
-// 16 rows bf16 27.3 / 25.6, FP8 27.1 / 36.4, FP4 42.2 / 40.4; 64 sequences of
-// 2048-6404 states: 4 rows bf16 165 / 204, FP8 107 / 326, FP4 138 / 393; 16 rows
-// bf16 186 / 209, FP8 155 / 329, FP4 223 / 394. It has registers for two tiles
-// of 8 columns and no more.
+// heads of 128, us: 4 rows bf16 21.2 / 25.7, FP8 18.9 / 36.3, FP4 23.6 / 40.8;
+// 16 rows bf16 27.1 / 26.1, FP8 27.0 / 37.0, FP4 42.8 / 40.9; 64 sequences of
+// 2048-6404 states: 4 rows bf16 163 / 201, FP8 104 / 308, FP4 137 / 363; 16 rows
+// bf16 184 / 203, FP8 154 / 312, FP4 222 / 365. So 16 rows of few sequences lose
+// 4-5% to the other kernel over bf16 and FP4, and win elsewhere. It has registers
+// for two tiles of 8 columns and no more.
 constexpr int kFewColumns = 16;
 
 struct CrossParams {

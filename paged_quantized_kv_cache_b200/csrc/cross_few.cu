@@ -17,8 +17,9 @@
 // start and end hide behind the other's stream.
 //
 // Measured (32 / 8 heads of 128, one token each): 64 sequences of 2048-6404
-// states bf16 164 us (6.75 TB/s), FP8 106-112 us (5.0-5.3 TB/s, bound by the
-// dequantization's instructions); 16 of 1400-1500 bf16 states 20.9 us.
+// states bf16 163 us (6.8 TB/s), FP8 104-110 us (5.1-5.3 TB/s, bound by the
+// dequantization's instructions), FP4 137 us (2.5 TB/s, bound by them too); 16 of
+// 1400-1500 bf16 states 21.2 us.
 #include <atomic>
 #include <climits>
 

@@ -76,7 +76,11 @@ enum { kSrcPlain = 0, kSrcRopeHalf = 1, kSrcRopeInterleaved = 2 };
 
 // The run's rows (tokens ts .. ts + n - 1 of KV head h, K or V) as 16-bit values
 // in this warp's shared rows: keys through norm_rotate and rounded, as
-// qk_norm_rope leaves them, values as they are.
+// qk_norm_rope leaves them, values as they are. Each KV head's warp reads the
+// tokens' angles for itself. With the queries' kernel, against qk_norm_rope and
+// kv_cache_write of contiguous values, us: 64 tokens, 32 / 8 heads of 128, FP8
+// 13.3 / 8.8, FP4 12.0 / 7.3; 8191 tokens FP8 139 / 89, FP4 148 / 92: this way
+// saves the copies of keys and values, not time.
 template <int D, bool BF16, int SRC>
 __device__ __forceinline__ void stage_run(const WriteParams& p, int ts, int n, int h, int kv, int lane,
                                           uint16_t* rows) {
