@@ -58,11 +58,13 @@ def binding_target() -> str:
     return "for python %d.%d, torch %s" % (*sys.version_info[:2], torch.__version__)
 
 
-def _binding_stale() -> bool:
-    if _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pqkv.h"), __file__]):
-        return True
+def _binding_fits() -> bool:
     with open(BINDING, "rb") as f:
-        return binding_target().encode() + b"\0" not in f.read()
+        return binding_target().encode() + b"\0" in f.read()
+
+
+def _binding_stale() -> bool:
+    return _stale(BINDING, [BINDING_SRC, os.path.join(ROOT, "include", "pqkv.h"), __file__]) or not _binding_fits()
 
 
 def _binding_command(out: str):
