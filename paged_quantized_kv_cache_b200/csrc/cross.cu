@@ -27,8 +27,8 @@
 // has a max from earlier tiles. That max then stays: exponents are taken against
 // it while the scores arrive, 16 columns (a cache block) at a time, without a
 // max of the tile, and only a row sum that shows a much larger score (f16 P:
-// 2^15, bf16 P: 2^30) takes the tile again the
-// general way: masks, max, rescaling of O and l. With H = 2 the warps of a row's
+// 2^15, bf16 P: 2^30) takes the tile again the general way: masks, max,
+// rescaling of O and l. With H = 2 the warps of a row's
 // two groups hand P over in the order of the tiles (a turn per 32 rows): the
 // max is shared, and a warp whose turn comes after the max was moved takes its
 // tile again.

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(FewGeom<KVF, D, NT>::kThreads, 2)
     float fc[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) fc[nt][0] = fc[nt][1] = 1.f;
-    // FP8: p is at most 2^8 (kLazy), so p s r stays below 2^15 unless
+    // FP8: p is at most 2^8 (kLazy), so p s r stays within f16 as long as no s r is above 2^7
     if constexpr (Gm::kFp8) grows |= fmaxf(use[0] ? sv[0] : 0.f, use[1] ? sv[1] : 0.f) * units > 128.f;
     if (__any_sync(kFull, grows)) {
 #pragma unroll
